@@ -304,6 +304,107 @@ int tpf_mlp_sp(tpf_handle h, int p, int64_t S, int64_t Hd, int64_t F, const void
                void* const* Y_slices, int y_dtype, int n_chunks, int sched, void* ws, size_t ws_bytes,
                void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The MLP block around its matrix products: norms, 8-bit activations, 4-bit
+ * weights.  Conventions as above; each call enqueues on `stream` only, keeps
+ * nothing between calls and can be captured in a graph.
+ * ------------------------------------------------------------------------- */
+
+/* Gate of tpf_block_norm. */
+#define TPF_GATE_NONE 0
+#define TPF_GATE_CHANNEL 1       /* gate[H]: one factor per channel */
+#define TPF_GATE_TOKEN 2         /* gate[M]: one factor per row */
+
+/* Largest row of tpf_block_norm (a row is held in one workgroup's registers). */
+#define TPF_NORM_MAX_H 32768
+
+/* Norms after and before a block, with its gate, residual scale and residual
+ * add, in one pass.  For every row:
+ *   b      = (blocks[0] + blocks[1]) + ... + blocks[p-1]      fp32
+ *   n      = b * (mean(b^2) + eps)^-1/2 * (w_post + o)
+ *   x_out  = alpha * x + beta * gate * n      rounded once to x_dtype
+ *   y      = x_out * (mean(x_out^2) + eps)^-1/2 * (w_pre + o)   bf16, of the
+ *            stored x_out: the next block's input
+ * with o = 1 if unit_offset (weights stored as offsets from 1), else 0.
+ *   x, x_out: [M, H] of x_dtype; x_out may be x itself (updated in place).
+ *   blocks[k]: [M, H] of b_dtype: the block's output (p = 1) or its p shards'
+ *   partial sums (the AllReduce is then part of this call).
+ *   w_pre, w_post: [H], gate: per gate_kind (NULL for TPF_GATE_NONE), all of
+ *   w_dtype.  y: [M, H] bf16.
+ *   stats: NULL, or [2, M] fp32: both reciprocal roots, for the backward.
+ * H must be a multiple of 8 and at most TPF_NORM_MAX_H.  Results do not depend
+ * on the other rows. */
+int tpf_block_norm(tpf_handle h, int p, int64_t M, int64_t H, const void* x, int x_dtype,
+                   const void* const* blocks, int b_dtype, const void* w_pre, const void* w_post,
+                   const void* gate, int gate_kind, int w_dtype, float alpha, float beta, float eps,
+                   int unit_offset, void* x_out, void* y, float* stats, void* stream);
+
+/* Bytes of workspace of tpf_block_norm_backward (0 for invalid sizes). */
+size_t tpf_block_norm_backward_ws(int64_t M, int64_t H);
+
+/* Backward of tpf_block_norm, given its inputs and x_out and stats:
+ *   dy: [M, H] bf16, the gradient of y; dx_out: [M, H] of x_dtype, the gradient
+ *   of x_out from what reads it besides y (NULL: none); x: the x_out of the
+ *   forward; stats: the forward's.
+ *   dx: [M, H] of x_dtype, the gradient of x; db: [M, H] bf16, the gradient of
+ *   each of blocks[k] (they share it); dw_pre, dw_post: [H] fp32; dgate: fp32,
+ *   of the gate's shape (NULL for TPF_GATE_NONE).
+ * Column sums are added in an order fixed by M and H alone: the same bits at
+ * every call.  Outputs must not alias inputs. */
+int tpf_block_norm_backward(tpf_handle h, int p, int64_t M, int64_t H, const void* dy, const void* dx_out,
+                            const void* x, int x_dtype, const void* const* blocks, int b_dtype,
+                            const float* stats, const void* w_pre, const void* w_post, const void* gate,
+                            int gate_kind, int w_dtype, float alpha, float beta, int unit_offset, void* dx,
+                            void* db, float* dw_pre, float* dw_post, float* dgate, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Activations in 8 bits.  u[k] [M, F] bf16 is cut into blocks of 32 x 32 (the
+ * last ones may be smaller); scales[k] [ceil(M/32), ceil(F/32)] holds one byte
+ * e a block, the factor 2^(e-127): the least one, not below 2^-117, that keeps
+ * the block's largest finite magnitude within 448 of it.  codes[k] [M, F] are
+ * OCP e4m3 values of u 2^(127-e), rounded to nearest even, and NaN where u is
+ * not finite.  With gelu != 0 the same pass writes h[k] [M, F] bf16 =
+ * GeLU(u) (erf form, fp32, rounded once); otherwise h is ignored.
+ * F must be a multiple of 8; codes are 8-byte aligned, scales any byte. */
+int tpf_stash_pack(tpf_handle h, int p, int64_t M, int64_t F, const void* const* u, int gelu, void* const* act,
+                   void* const* codes, void* const* scales, void* stream);
+
+/* GeLU's gradient from the 8-bit activations: with u = code * 2^(e-127) and
+ * Phi, phi the normal distribution and density,
+ *   du[k] = dh[k] (Phi(u) + u phi(u)),  act[k] = u Phi(u)      bf16, [M, F]. */
+int tpf_stash_backward(tpf_handle h, int p, int64_t M, int64_t F, const void* const* codes,
+                       const void* const* scales, const void* const* dh, void* const* du, void* const* act,
+                       void* stream);
+
+/* Weight gradients from 8-bit activations: dW[k] = U_k^T dY[k] with U_k
+ * [M, R] the values of codes[k] and scales[k] (exact in bf16), dY[k] [M, C]
+ * bf16, dW[k] [R, C] of dw_dtype; sums over the M rows in fp32.  R and C must
+ * be multiples of 8.  As tpf_weight_grad otherwise. */
+int tpf_stash_weight_grad(tpf_handle h, int p, int64_t M, int64_t R, int64_t C, const void* const* codes,
+                          const void* const* scales, const void* const* dY, void* const* dW, int dw_dtype,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of tpf_stash_weight_grad (0: none needed, or invalid sizes). */
+size_t tpf_stash_weight_grad_ws(int p, int64_t M, int64_t R, int64_t C);
+
+/* Products with 4-bit weights: Y = sum_k X[k] W_k^T, the row-parallel Linear
+ * (p = 1: any Linear) of a decode step.
+ *   X[k]: [M, K] bf16.
+ *   codes[k]: [N, K/2] bytes; of every four bytes, byte j holds code j of a run
+ *   of eight in its low half and code j + 4 in its high half.
+ *   scales[k]: [N, K/group] bf16; zeros[k]: [N, K/group] bytes, or zeros NULL:
+ *   8 everywhere.  W_k[n][j] = (code - zero) * scale of its group.
+ *   Y: [M, N] of y_dtype; with gelu != 0 GeLU of the fp32 sum.
+ * group is 32, 64 or 128 and divides K; N is any positive number.  Weights are
+ * read once for every 64 rows of X.  Sums are fp32, in an order fixed by the
+ * sizes.  scales need 2-byte alignment, zeros none. */
+int tpf_qweight_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, int group, const void* const* X,
+                       const void* const* codes, const void* const* scales, const void* const* zeros, int gelu,
+                       void* Y, int y_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of tpf_qweight_matmul (0: none needed, or invalid sizes). */
+size_t tpf_qweight_matmul_ws(int p, int64_t M, int64_t K, int64_t N, int group);
+
 /* Wait for the handle's work on `stream` to finish and report whether a
  * bounded wait inside the persistent kernel gave up since the last query
  * (TPF_ERR_TIMEOUT; the outputs of that call are then undefined).  Clears

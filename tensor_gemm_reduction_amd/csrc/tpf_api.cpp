@@ -15,6 +15,7 @@
 #include <string>
 
 #include "../../include/tpfuse.h"
+#include "tpf_host.hpp"
 #include "tpf_internal.hpp"
 #include "tpf_stationary.hpp"
 
@@ -22,8 +23,6 @@ using namespace tpf;
 
 static_assert(TPF_MAX_SHARDS == kMaxShards, "shard limit mismatch");
 static_assert(TPF_MAX_CHUNKS == kMaxChunks, "chunk limit mismatch");
-
-constexpr int kKernelTimes = 256;   // debug kernel-timing records held per handle
 
 // Partial workspace of tpf_matmul_allreduce_noalloc: a file-scope device
 // array, one copy per GPU the library runs on, held until the process ends.
@@ -47,55 +46,11 @@ void* g_scratch_ptr[kMaxDevices] = {};
 // were slower).
 constexpr int kSideReduceCuDiv = 4;
 
-struct tpf_context {
-  int device = 0;
-  int num_cus = 0;
-  hipStream_t side = nullptr;           // reductions (reducing ops) or gather copies (AllGather)
-  hipStream_t gemm2 = nullptr;          // every other chunk's GEMM (two-stream scheduler)
-  hipEvent_t ev_fork = nullptr, ev_join = nullptr, ev_join2 = nullptr;
-  hipEvent_t ev_chunk[kMaxChunks] = {};
-  hipEvent_t ev_slice[kMaxShards] = {};
-  Ctrl* ctrl = nullptr;
-  int* tile_cnt = nullptr;             // kTileCounters per-output-tile counters (tile scheduler)
-  int64_t spin_limit = 0;
-  int unreachable = 0;
-  TimelineEvent* timeline = nullptr;   // caller-owned device buffer (debug)
-  int timeline_cap = 0;
-  // Debug kernel timing: a ring of timing-event pairs around each call's
-  // dominant launch.
-  bool ktime = false;
-  hipEvent_t kt0[kKernelTimes] = {}, kt1[kKernelTimes] = {};
-  int kt_next = 0;      // ring slot of the next record
-  int kt_count = 0;     // records held (<= kKernelTimes)
-  int last_sched = -1;  // scheduler the last call ran (AUTO resolved), -1 before any
-  void* scratch = nullptr;  // this device's copy of the no-allocation workspace
-  DelayArgs delay{};        // debug: timing perturbation of the producers (tpf_debug_set_delay)
-};
-
 namespace {
 
 // Polls before a bounded wait gives up (polls back off to ~4K clocks each,
 // so this is a few seconds: far beyond any legitimate wait).
 constexpr int64_t kDefaultSpinLimit = (int64_t)1 << 21;
-
-thread_local std::string g_last_error;
-
-int fail(int code, const std::string& msg) {
-  g_last_error = msg;
-  return code;
-}
-
-int hip_fail(hipError_t e, const char* what) {
-  return fail(TPF_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
-#define TPF_HIP(call)                                  \
-  do {                                                 \
-    hipError_t e_ = (call);                            \
-    if (e_ != hipSuccess) return hip_fail(e_, #call);  \
-  } while (0)
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // A scheduler id in the low byte, optionally OR-ed with TPF_MSG_BF16.
 bool valid_sched(int s) {
@@ -103,9 +58,6 @@ bool valid_sched(int s) {
   return base >= TPF_SCHED_AUTO && base <= TPF_SCHED_STATIONARY && (flags & ~TPF_MSG_BF16) == 0;
 }
 bool msg_bf16(int s) { return (s & TPF_MSG_BF16) != 0; }
-bool valid_dtype(int d) { return d == TPF_BF16 || d == TPF_F32; }
-
-int out_kind(int dtype) { return dtype == TPF_F32 ? OUT_F32 : OUT_BF16; }
 
 // Tile configuration from the op's total row count only (never from the
 // chunking): every configuration runs the same MFMA sequence per element, so
@@ -132,22 +84,6 @@ int check_common(int p, int64_t M, int64_t N, int64_t K, int n_chunks, int dtype
   return TPF_OK;
 }
 
-int check_ptrs(const void* const* arr, int count, const char* name) {
-  if (!arr) return fail(TPF_ERR_INVALID_ARG, std::string(name) + " array is NULL");
-  for (int i = 0; i < count; ++i) {
-    if (!arr[i]) return fail(TPF_ERR_INVALID_ARG, std::string(name) + "[" + std::to_string(i) + "] is NULL");
-    if (!aligned16(arr[i]))
-      return fail(TPF_ERR_ALIGNMENT, std::string(name) + "[" + std::to_string(i) + "] is not 16-byte aligned");
-  }
-  return TPF_OK;
-}
-
-int check_ptr(const void* ptr, const char* name) {
-  if (!ptr) return fail(TPF_ERR_INVALID_ARG, std::string(name) + " is NULL");
-  if (!aligned16(ptr)) return fail(TPF_ERR_ALIGNMENT, std::string(name) + " is not 16-byte aligned");
-  return TPF_OK;
-}
-
 // Workspace of the reducing ops: one local output ("message") per shard,
 // fp32 or (TPF_MSG_BF16) bf16.  The output-stationary scheduler keeps the
 // partials on chip and needs none for weights stored [K][N] (the
@@ -156,20 +92,6 @@ int check_ptr(const void* ptr, const char* name) {
 size_t partial_bytes(int p, int64_t M, int64_t N, int sched, bool weights_kn = false) {
   if ((sched & 0xff) == TPF_SCHED_STATIONARY && (weights_kn || pick_cfg(M) == CFG_LARGE)) return 0;
   return (size_t)p * (size_t)M * (size_t)N * (msg_bf16(sched) ? 2 : 4);
-}
-
-int check_ws(void* ws, size_t ws_bytes, size_t need) {
-  if (need == 0) return TPF_OK;
-  if (!ws) return fail(TPF_ERR_WORKSPACE, "workspace is NULL but " + std::to_string(need) + " bytes are needed");
-  if (!aligned16(ws)) return fail(TPF_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
-  if (ws_bytes < need)
-    return fail(TPF_ERR_WORKSPACE, "workspace has " + std::to_string(ws_bytes) + " bytes, needs " + std::to_string(need));
-  return TPF_OK;
-}
-
-int check_handle(tpf_handle h) {
-  if (!h) return fail(TPF_ERR_INVALID_ARG, "handle is NULL");
-  return TPF_OK;
 }
 
 // AUTO.  The M027 page makes fusion conditional: measure the whole GEMM and
@@ -224,34 +146,6 @@ struct ReduceCall {
   int n_chunks, sched;
   void* P;                      // partials: fp32, or bf16 when ro.pbf16
 };
-
-int set_device(tpf_handle h) {
-  TPF_HIP(hipSetDevice(h->device));
-  return TPF_OK;
-}
-
-// Debug kernel timing: record the start / stop event of the current call's
-// dominant launch on the stream it is launched on.
-int ktime_start(tpf_handle h, hipStream_t s) {
-  if (h->ktime) TPF_HIP(hipEventRecord(h->kt0[h->kt_next], s));
-  return TPF_OK;
-}
-int ktime_stop(tpf_handle h, hipStream_t s) {
-  if (!h->ktime) return TPF_OK;
-  TPF_HIP(hipEventRecord(h->kt1[h->kt_next], s));
-  h->kt_next = (h->kt_next + 1) % kKernelTimes;
-  h->kt_count = std::min(h->kt_count + 1, kKernelTimes);
-  return TPF_OK;
-}
-
-#define TPF_TIMED(h, s, launch)      \
-  do {                               \
-    int st_ = ktime_start((h), (s)); \
-    if (st_) return st_;             \
-    TPF_HIP(launch);                 \
-    st_ = ktime_stop((h), (s));      \
-    if (st_) return st_;             \
-  } while (0)
 
 // The fold scheduler's two launches over output rows [row0, row1): shards
 // 0..p-2 into their partials, then shard p-1, whose epilogue adds those

@@ -1,0 +1,93 @@
+// The MLP block's operators around its matrix products: the norms before and
+// after it, its activations kept in 8 bits, its products with 4-bit weights.
+// Plain structs passed by value as kernel arguments.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "tpf_device.hpp"
+#include "tpf_internal.hpp"
+
+namespace tpf {
+
+enum GateKind : int { GATE_NONE = 0, GATE_CHANNEL = 1, GATE_TOKEN = 2 };
+
+constexpr int kNormMaxH = 32768;     // a row is held in one workgroup's registers
+constexpr int kStashBlock = 32;      // 8-bit activations: one scale per 32 x 32 values
+constexpr int kQwMaxRows = 64;       // rows of X one workgroup of the 4-bit product holds
+
+// ---------------------------------------------------------------------------
+// Norms.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  const void* x;                     // [M][H] residual stream (backward: after the block)
+  const void* blocks[kMaxShards];    // [M][H] each: the block's output, or its p partial sums
+  const void* w_pre;                 // [H]
+  const void* w_post;                // [H]
+  const void* gate;                  // [H], [M] or NULL
+  void* x_out;                       // forward: [M][H]; backward: dx
+  void* y;                           // forward: [M][H] bf16; backward: db
+  float* stats;                      // [2][M]: 1/rms of the block's output, then of x_out (forward: may be NULL)
+  const void* dy;                    // backward: [M][H] bf16
+  const void* dx_out;                // backward: [M][H] (NULL: zeros)
+  float* dw_pre;                     // backward: [H]
+  float* dw_post;                    // backward: [H]
+  float* dgate;                      // backward: [H], [M] or NULL
+  float* partial;                    // backward: [groups][2][H] column sums
+  int p, M, H;
+  int x_f32, b_f32, w_f32;           // 1: fp32, 0: bf16
+  int gate_kind;
+  float alpha, beta, eps, offset;    // offset: 1 where the weights are stored as offsets from 1
+  int groups;                        // backward: workgroups, each summing rows group, group + groups, ...
+};
+
+// Workgroups of the backward's row pass: a pure function of M and H.
+int norm_backward_groups(int64_t M, int64_t H);
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_block_norm_backward(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_columns(const NormArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Activations in 8 bits: e4m3 codes [M][F] and one power of two (its binary32
+// exponent byte) per 32 x 32 block, [ceil(M / 32)][ceil(F / 32)].
+// ---------------------------------------------------------------------------
+struct StashArgs {
+  const void* u[kMaxShards];         // pack: [M][F] bf16
+  void* h[kMaxShards];               // [M][F] bf16: GeLU(u) (pack without GeLU: unused)
+  uint8_t* codes[kMaxShards];
+  uint8_t* scales[kMaxShards];
+  const void* dh[kMaxShards];        // backward: [M][F] bf16
+  void* du[kMaxShards];              // backward: [M][F] bf16
+  int p, M, F;
+};
+hipError_t launch_stash_pack(const StashArgs& a, int gelu, int num_cus, hipStream_t s);
+hipError_t launch_stash_backward(const StashArgs& a, int num_cus, hipStream_t s);
+
+struct StashGradArgs {
+  const uint8_t* codes[kMaxShards];  // [M][R]
+  const uint8_t* scales[kMaxShards];
+  const __bf16* dY[kMaxShards];      // [M][C]
+  void* dW[kMaxShards];              // [R][C]
+  int p, M, R, C;
+  int out;                           // OUT_F32 or OUT_BF16
+  int tiles_m, tiles_n, tasks;
+};
+hipError_t launch_stash_weight_grad(StashGradArgs a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// 4-bit weights: W_k[n][j] = (q - z) * s with one scale s (bf16) and zero
+// point z (one byte, or 8 everywhere) per `group` consecutive j of a row.
+// ---------------------------------------------------------------------------
+struct QweightArgs {
+  const __bf16* X[kMaxShards];       // [M][K]
+  const uint8_t* codes[kMaxShards];  // [N][K / 2]
+  const uint16_t* scales[kMaxShards];  // [N][K / group] bf16
+  const uint8_t* zeros[kMaxShards];  // [N][K / group], or NULL: 8
+  void* Y;                           // [M][N]
+  int p, M, K, N, group;
+  int gelu, out;
+};
+hipError_t launch_qweight(const QweightArgs& a, hipStream_t s);
+
+}  // namespace tpf

@@ -1,0 +1,228 @@
+// Activations kept in 8 bits for the backward pass: pack (with the forward's
+// GeLU), GeLU's gradient and the weight gradient that read them.
+//
+// A block of 32 x 32 values shares the least power of two s >= 2^-117 with
+// max|finite u| <= 448 s; codes are e4m3(u / s), round to nearest even, and
+// NaN where u is not finite.  s >= 2^-117 makes code * s a normal bf16 or
+// zero, so every stored value is exact in bf16.
+#include <algorithm>
+
+#include "tpf_block.hpp"
+
+namespace tpf {
+
+typedef u32x2_t u32x2a4_t __attribute__((aligned(4)));   // codes rows are 8-byte aligned at least
+
+template <class A>
+__device__ __forceinline__ const A& stash_kernarg() {
+  return *(const A*)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
+// Phi(-a) / exp(-a^2 / 2) for a >= 0 as a polynomial in 1 / (1 + 0.31 a),
+// fitted here to the least largest relative error over [0, 14]: 4.8e-6, far
+// below half a bf16 step (2^-9).  One reciprocal and one exp2 serve the value
+// and the density, where erff and expf took about twice the instructions.
+struct Gauss {
+  float cdf;      // Phi(u)
+  float bell;     // exp(-u^2 / 2)
+};
+__device__ __forceinline__ Gauss gauss(float u) {
+  const float a = fabsf(u);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31f, a, 1.0f));
+  float q = -0.0739293803f;
+  q = __builtin_fmaf(q, t, 0.180450903f);
+  q = __builtin_fmaf(q, t, 0.0157443031f);
+  q = __builtin_fmaf(q, t, 0.133429849f);
+  q = __builtin_fmaf(q, t, 0.12044131f);
+  q = __builtin_fmaf(q, t, 0.123860693f);
+  const float bell = __builtin_amdgcn_exp2f(u * u * -0.72134752044f);
+  const float tail = q * t * bell;
+  return Gauss{u < 0.0f ? tail : 1.0f - tail, bell};
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const bf16x2_t v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// One wave packs 32 rows x 128 columns: lane l holds the eight columns
+// 8 (l % 16) of rows l / 16 + 4 i, so a 32-column block is four lanes wide and
+// its largest value takes the lane's own maximum and four exchanges.
+template <int GELU>
+__global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
+  (void)args;
+  const StashArgs& a = stash_kernarg<StashArgs>();
+  const int lane = threadIdx.x & 63;
+  const int strips = (a.F + 127) / 128, bands = (a.M + 31) / 32;
+  const int nsc = (a.F + 31) / 32;
+  const int64_t units = (int64_t)strips * bands;
+  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (unit >= units * a.p) return;
+  const int k = __builtin_amdgcn_readfirstlane((int)(unit / units));
+  const int64_t r = unit - k * units;
+  const int band = (int)(r / strips), strip = (int)(r % strips);
+  const int col = strip * 128 + (lane & 15) * 8;
+  const int row0 = band * 32 + (lane >> 4);
+  const uint16_t* u = reinterpret_cast<const uint16_t*>(a.u[k]);
+  const bool cok = col < a.F;
+  u32x4_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 4 * i;
+    w[i] = u32x4_t{0, 0, 0, 0};
+    if (cok && row < a.M) w[i] = *reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.F + col);
+  }
+  // Largest finite magnitude, as bf16 bits.
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = w[i][j] & 0x7fffu, hi = (w[i][j] >> 16) & 0x7fffu;
+      if (lo < 0x7f80u) top = max(top, lo);
+      if (hi < 0x7f80u) top = max(top, hi);
+    }
+#pragma unroll
+  for (int d = 1; d <= 32; d <<= 1)
+    if (d != 4 && d != 8) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+  // The exponent byte of the least power of two that brings the largest value
+  // to 448 = 1.75 2^8 or below (one more above 1.75); at least 2^-117.
+  const int e = max(10, (int)(((top << 16) + 0x1fffffu) >> 23) - 8);
+  const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = row0 + 4 * i;
+    if (!cok || row >= a.M) continue;
+    u32x2_t c;
+    u32x4_t hv;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float lo = bf_lo(w[i][j]), hi = bf_hi(w[i][j]);
+      int two = __builtin_amdgcn_cvt_pk_fp8_f32(lo * inv, hi * inv, 0, false) & 0xffff;
+      if ((w[i][j] & 0x7f80u) == 0x7f80u) two = (two & 0xff00) | 0x7f;
+      if ((w[i][j] & 0x7f800000u) == 0x7f800000u) two = (two & 0x00ff) | 0x7f00;
+      if (j & 1) c[j >> 1] |= (uint32_t)two << 16;
+      else c[j >> 1] = (uint32_t)two;
+      if constexpr (GELU) hv[j] = pack_bf16(lo * gauss(lo).cdf, hi * gauss(hi).cdf);
+    }
+    const int64_t at = (int64_t)row * a.F + col;
+    *reinterpret_cast<u32x2a4_t*>(a.codes[k] + at) = c;
+    if constexpr (GELU) *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.h[k]) + at) = hv;
+  }
+  if (cok && (lane & 51) == 0) a.scales[k][(int64_t)band * nsc + (col >> 5)] = (uint8_t)e;
+}
+
+hipError_t launch_stash_pack(const StashArgs& a, int gelu, int num_cus, hipStream_t s) {
+  (void)num_cus;
+  const int64_t units = (int64_t)((a.F + 127) / 128) * ((a.M + 31) / 32) * a.p;
+  const dim3 grid((unsigned)((units + 3) / 4));
+  if (gelu) hipLaunchKernelGGL(stash_pack_kernel<1>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(stash_pack_kernel<0>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// du = dh (Phi(u) + u phi(u)) and h = u Phi(u) from the stored values, eight
+// columns a lane.
+__global__ __launch_bounds__(256) void stash_backward_kernel(StashArgs args) {
+  (void)args;
+  const StashArgs& a = stash_kernarg<StashArgs>();
+  const int k = blockIdx.y;
+  const int fv = a.F / 8, nsc = (a.F + 31) / 32;
+  const int64_t total = (int64_t)a.M * fv;
+  const uint8_t* codes = a.codes[k];
+  const uint8_t* scales = a.scales[k];
+  const uint16_t* dh = reinterpret_cast<const uint16_t*>(a.dh[k]);
+  uint16_t* du = reinterpret_cast<uint16_t*>(a.du[k]);
+  uint16_t* h = reinterpret_cast<uint16_t*>(a.h[k]);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int row = (int)(i / fv), v = (int)(i - (int64_t)row * fv);
+    const u32x2_t c = *reinterpret_cast<const u32x2a4_t*>(codes + i * 8);
+    const u32x4_t g = *reinterpret_cast<const u32x4_t*>(dh + i * 8);
+    const float scale = __uint_as_float((uint32_t)scales[(int64_t)(row >> 5) * nsc + (v >> 2)] << 23);
+    u32x4_t o, y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      typedef float f32x2_t __attribute__((ext_vector_type(2)));
+      const f32x2_t two = (j & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j >> 1], true)
+                                  : __builtin_amdgcn_cvt_pk_f32_fp8((int)c[j >> 1], false);
+      const float u0 = two[0] * scale, u1 = two[1] * scale;
+      const Gauss g0 = gauss(u0), g1 = gauss(u1);
+      const float d0 = bf_lo(g[j]) * __builtin_fmaf(u0 * 0.3989422804f, g0.bell, g0.cdf);
+      const float d1 = bf_hi(g[j]) * __builtin_fmaf(u1 * 0.3989422804f, g1.bell, g1.cdf);
+      o[j] = pack_bf16(d0, d1);
+      y[j] = pack_bf16(u0 * g0.cdf, u1 * g1.cdf);
+    }
+    *reinterpret_cast<u32x4_t*>(du + i * 8) = o;
+    *reinterpret_cast<u32x4_t*>(h + i * 8) = y;
+  }
+}
+
+hipError_t launch_stash_backward(const StashArgs& a, int num_cus, hipStream_t s) {
+  const int64_t groups = ((int64_t)a.M * (a.F / 8) + 255) / 256;
+  const int64_t cap = std::max<int64_t>(1, (int64_t)num_cus * 32 / a.p);
+  hipLaunchKernelGGL(stash_backward_kernel, dim3((unsigned)std::min(groups, cap), (unsigned)a.p), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// dW_k = U_k^T dY_k, U = code * scale.  64 x 64 output tiles of four waves,
+// each a 32 x 32 block; 16 rows of the contraction a step through LDS,
+// transposed as they are written.
+constexpr int kSgTile = 64;
+__global__ __launch_bounds__(256) void stash_grad_kernel(StashGradArgs args) {
+  (void)args;
+  const StashGradArgs& a = stash_kernarg<StashGradArgs>();
+  __shared__ __bf16 ua[kSgTile][24], yb[kSgTile][24];   // [column][row of the step], padded
+  const int per = a.tiles_m * a.tiles_n;
+  const int k = blockIdx.x / per, t = blockIdx.x % per;
+  const int r0 = (t / a.tiles_n) * kSgTile, c0 = (t % a.tiles_n) * kSgTile;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wr = (wave >> 1) * 32, wc = (wave & 1) * 32;
+  const int nsc = (a.R + 31) / 32;
+  const int col = threadIdx.x & 63, rs = threadIdx.x >> 6;    // loader: one column, rows rs + 4 i
+  f32x16_t acc;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+  for (int m0 = 0; m0 < a.M; m0 += 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = m0 + rs + 4 * i;
+      __bf16 u = (__bf16)0.0f, y = (__bf16)0.0f;
+      if (row < a.M && r0 + col < a.R) {
+        const float scale =
+            __uint_as_float((uint32_t)a.scales[k][(int64_t)(row >> 5) * nsc + ((r0 + col) >> 5)] << 23);
+        u = (__bf16)(__builtin_amdgcn_cvt_f32_fp8((int)a.codes[k][(int64_t)row * a.R + r0 + col], 0) * scale);
+      }
+      if (row < a.M && c0 + col < a.C) y = a.dY[k][(int64_t)row * a.C + c0 + col];
+      ua[col][rs + 4 * i] = u;
+      yb[col][rs + 4 * i] = y;
+    }
+    __syncthreads();
+    const bf16x8_t av = *reinterpret_cast<const bf16x8_t*>(&ua[wr + (lane & 31)][(lane >> 5) * 8]);
+    const bf16x8_t bv = *reinterpret_cast<const bf16x8_t*>(&yb[wc + (lane & 31)][(lane >> 5) * 8]);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, bv, acc, 0, 0, 0);
+    __syncthreads();
+  }
+  const int c = c0 + wc + (lane & 31);
+#pragma unroll
+  for (int v = 0; v < 16; ++v) {
+    const int r = r0 + wr + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+    if (r < a.R && c < a.C) {
+      const int64_t at = (int64_t)r * a.C + c;
+      if (a.out == OUT_F32) reinterpret_cast<float*>(a.dW[k])[at] = acc[v];
+      else reinterpret_cast<__bf16*>(a.dW[k])[at] = (__bf16)acc[v];
+    }
+  }
+}
+
+hipError_t launch_stash_weight_grad(StashGradArgs a, hipStream_t s) {
+  a.tiles_m = (a.R + kSgTile - 1) / kSgTile;
+  a.tiles_n = (a.C + kSgTile - 1) / kSgTile;
+  a.tasks = a.p * a.tiles_m * a.tiles_n;
+  hipLaunchKernelGGL(stash_grad_kernel, dim3((unsigned)a.tasks), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace tpf

@@ -25,6 +25,8 @@ BF16, F32 = 0, 1
  SCHED_FOLD, SCHED_STATIONARY) = range(9)
 ALLREDUCE, REDUCESCATTER = 0, 1
 OP_MATMUL_ALLREDUCE, OP_MATMUL_REDUCESCATTER, OP_ALLGATHER_MATMUL, OP_MATMUL_DX, OP_MLP_SP = range(5)
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
+NORM_MAX_H = 32768
 MAX_SHARDS = 16
 MAX_CHUNKS = 64
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -38,6 +40,7 @@ _PP = ctypes.POINTER(ctypes.c_void_p)
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 # name -> (restype, argtypes); the set of exported functions of include/tpfuse.h
 SIGNATURES = {
@@ -51,6 +54,17 @@ SIGNATURES = {
     "tpf_matmul_dx": (_I, [_VP, _I, _I, _I64, _I64, _I64, _PP, _PP, _PP, _I, _I, _I, _VP, _SZ, _VP]),
     "tpf_weight_grad": (_I, [_VP, _I, _I64, _I64, _I64, _PP, _PP, _PP, _I, _VP]),
     "tpf_mlp_sp": (_I, [_VP, _I, _I64, _I64, _I64, _PP, _PP, _PP, _VP, _PP, _PP, _I, _I, _I, _VP, _SZ, _VP]),
+    "tpf_block_norm": (_I, [_VP, _I, _I64, _I64, _VP, _I, _PP, _I, _VP, _VP, _VP, _I, _I, _F, _F, _F, _I, _VP, _VP,
+                            _VP, _VP]),
+    "tpf_block_norm_backward_ws": (_SZ, [_I64, _I64]),
+    "tpf_block_norm_backward": (_I, [_VP, _I, _I64, _I64, _VP, _VP, _VP, _I, _PP, _I, _VP, _VP, _VP, _VP, _I, _I, _F,
+                                     _F, _I, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "tpf_stash_pack": (_I, [_VP, _I, _I64, _I64, _PP, _I, _PP, _PP, _PP, _VP]),
+    "tpf_stash_backward": (_I, [_VP, _I, _I64, _I64, _PP, _PP, _PP, _PP, _PP, _VP]),
+    "tpf_stash_weight_grad_ws": (_SZ, [_I, _I64, _I64, _I64]),
+    "tpf_stash_weight_grad": (_I, [_VP, _I, _I64, _I64, _I64, _PP, _PP, _PP, _PP, _I, _VP, _SZ, _VP]),
+    "tpf_qweight_matmul_ws": (_SZ, [_I, _I64, _I64, _I64, _I]),
+    "tpf_qweight_matmul": (_I, [_VP, _I, _I64, _I64, _I64, _I, _PP, _PP, _PP, _PP, _I, _VP, _I, _VP, _SZ, _VP]),
     "tpf_sync_status": (_I, [_VP, _VP]),
     "tpf_debug_set_wait": (_I, [_VP, _I64, _I]),
     "tpf_debug_set_delay": (_I, [_VP, ctypes.c_uint32, _I, _I]),
@@ -522,3 +536,222 @@ def mlp_sp(X_slices: List[torch.Tensor], W1: List[torch.Tensor], W2: List[torch.
                             _sched(sched, message), ws.data_ptr() if ws is not None else None, ws_bytes,
                             _stream_ptr(stream)))
     return X_gathered, H, Y
+
+
+# ---------------------------------------------------------------------------
+# The MLP block around its matrix products.
+# ---------------------------------------------------------------------------
+
+STASH_BLOCK = 32
+CODE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _ptrs(ts):
+    return ptr_array([t.data_ptr() for t in ts])
+
+
+def _norm_operands(x, blocks, w_pre, w_post, gate):
+    """Checks shared by the norm's two directions; returns (device, M, H, gate kind)."""
+    p = len(blocks)
+    _need(p >= 1, "blocks: no tensors given")
+    _need(x.dim() == 2, f"x has {x.dim()} dimensions, expected [M, H]")
+    M, H = x.shape
+    dev = _check("x", [x], (M, H), OUT_DTYPES)
+    _check("blocks", blocks, (M, H), OUT_DTYPES, dev)
+    _need(all(b.dtype == blocks[0].dtype for b in blocks), "blocks: the tensors differ in dtype")
+    _check("w_pre", [w_pre], (H,), OUT_DTYPES, dev)
+    _check("w_post", [w_post], (H,), (w_pre.dtype,), dev)
+    kind = GATE_NONE
+    if gate is not None:
+        kind = GATE_TOKEN if gate.dim() == 2 else GATE_CHANNEL
+        _check("gate", [gate], (M, 1) if kind == GATE_TOKEN else (H,), (w_pre.dtype,), dev)
+    return dev, M, H, kind
+
+
+def block_norm(x: torch.Tensor, blocks: Sequence[torch.Tensor], w_pre: torch.Tensor, w_post: torch.Tensor,
+               gate: Optional[torch.Tensor] = None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+               unit_offset: bool = False, want_stats: bool = False, x_out: Optional[torch.Tensor] = None,
+               y: Optional[torch.Tensor] = None, handle: Optional[Handle] = None, stream=None):
+    """(x_out, y, stats): the norm after a block with its gate, residual scale
+    and residual add, and the norm before the next block, in one pass.
+
+        b     = blocks[0] + ... + blocks[p-1]
+        x_out = alpha x + beta gate rms_norm(b) w_post        (x's dtype; may be x itself)
+        y     = rms_norm(x_out) w_pre                         (bf16)
+
+    `gate` is None, [H] (one factor a channel) or [M, 1] (one a token); weights
+    are stored as offsets from 1 with `unit_offset`.  `stats` ([2, M] fp32, for
+    `block_norm_backward`) is None unless `want_stats`."""
+    dev, M, H, kind = _norm_operands(x, blocks, w_pre, w_post, gate)
+    with _on(stream):
+        if x_out is None:
+            x_out = torch.empty_like(x)
+        if y is None:
+            y = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        stats = torch.empty((2, M), dtype=torch.float32, device=dev) if want_stats else None
+    _check("x_out", [x_out], (M, H), (x.dtype,), dev)
+    _check("y", [y], (M, H), (torch.bfloat16,), dev)
+    h = _handle(handle, dev, stream)
+    check(load().tpf_block_norm(h.ptr, len(blocks), M, H, x.data_ptr(), _dtype_code(x.dtype), _ptrs(blocks),
+                                _dtype_code(blocks[0].dtype), w_pre.data_ptr(), w_post.data_ptr(),
+                                gate.data_ptr() if gate is not None else None, kind, _dtype_code(w_pre.dtype), alpha,
+                                beta, eps, 1 if unit_offset else 0, x_out.data_ptr(), y.data_ptr(),
+                                stats.data_ptr() if stats is not None else None, _stream_ptr(stream)))
+    return x_out, y, stats
+
+
+def block_norm_backward(dy: torch.Tensor, dx_out: Optional[torch.Tensor], x: torch.Tensor,
+                        blocks: Sequence[torch.Tensor], stats: torch.Tensor, w_pre: torch.Tensor,
+                        w_post: torch.Tensor, gate: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                        beta: float = 1.0, unit_offset: bool = False, ws: Optional[torch.Tensor] = None,
+                        handle: Optional[Handle] = None, stream=None):
+    """(dx, db, dw_pre, dw_post, dgate) of `block_norm`.
+
+    `dy` is the gradient of y, `dx_out` that of x_out from what else reads it
+    (None: nothing), `x` the forward's x_out, `stats` its statistics.  `db` is
+    the gradient of every tensor of `blocks`; `dgate` has the gate's shape."""
+    dev, M, H, kind = _norm_operands(x, blocks, w_pre, w_post, gate)
+    _check("dy", [dy], (M, H), (torch.bfloat16,), dev)
+    if dx_out is not None:
+        _check("dx_out", [dx_out], (M, H), (x.dtype,), dev)
+    _check("stats", [stats], (2, M), (torch.float32,), dev)
+    _check_ws(ws, dev)
+    need = load().tpf_block_norm_backward_ws(M, H)
+    with _on(stream):
+        dx = torch.empty_like(x)
+        db = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+        dw_pre = torch.empty(H, dtype=torch.float32, device=dev)
+        dw_post = torch.empty(H, dtype=torch.float32, device=dev)
+        dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev) if gate is not None else None
+        if ws is None:
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    h = _handle(handle, dev, stream)
+    check(load().tpf_block_norm_backward(
+        h.ptr, len(blocks), M, H, dy.data_ptr(), dx_out.data_ptr() if dx_out is not None else None, x.data_ptr(),
+        _dtype_code(x.dtype), _ptrs(blocks), _dtype_code(blocks[0].dtype), stats.data_ptr(), w_pre.data_ptr(),
+        w_post.data_ptr(), gate.data_ptr() if gate is not None else None, kind, _dtype_code(w_pre.dtype), alpha, beta,
+        1 if unit_offset else 0, dx.data_ptr(), db.data_ptr(), dw_pre.data_ptr(), dw_post.data_ptr(),
+        dgate.data_ptr() if dgate is not None else None, ws.data_ptr(), ws.numel() * ws.element_size(),
+        _stream_ptr(stream)))
+    return dx, db, dw_pre, dw_post, dgate
+
+
+def _stash_shape(M: int, F: int):
+    return -(-M // STASH_BLOCK), -(-F // STASH_BLOCK)
+
+
+def stash_pack(u: Sequence[torch.Tensor], gelu: bool = True, handle: Optional[Handle] = None, stream=None):
+    """(h, codes, scales): the activations u[k] ([M, F] bf16) in 8 bits, and
+    h[k] = GeLU(u[k]) (bf16) from the same pass (None without `gelu`).
+
+    Every 32 x 32 block shares one power of two, 2^(scales - 127); codes are
+    e4m3, so that u ~ codes * 2^(scales - 127)."""
+    p = len(u)
+    _need(p >= 1, "u: no shards given")
+    _need(u[0].dim() == 2, f"u[0] has {u[0].dim()} dimensions, expected [M, F]")
+    M, F = u[0].shape
+    dev = _check("u", u, (M, F))
+    with _on(stream):
+        codes = [torch.empty((M, F), dtype=torch.float8_e4m3fn, device=dev) for _ in range(p)]
+        scales = [torch.empty(_stash_shape(M, F), dtype=torch.uint8, device=dev) for _ in range(p)]
+        h = [torch.empty((M, F), dtype=torch.bfloat16, device=dev) for _ in range(p)] if gelu else None
+    hd = _handle(handle, dev, stream)
+    check(load().tpf_stash_pack(hd.ptr, p, M, F, _ptrs(u), 1 if gelu else 0, _ptrs(h) if gelu else None,
+                                _ptrs(codes), _ptrs(scales), _stream_ptr(stream)))
+    return h, codes, scales
+
+
+def _check_stash(codes, scales):
+    p = len(codes)
+    _need(p >= 1, "codes: no shards given")
+    _need(codes[0].dim() == 2, f"codes[0] has {codes[0].dim()} dimensions, expected [M, F]")
+    M, F = codes[0].shape
+    _check_shards("scales", scales, p)
+    dev = _check("codes", codes, (M, F), CODE_DTYPES)
+    _check("scales", scales, _stash_shape(M, F), (torch.uint8,), dev)
+    return dev, p, M, F
+
+
+def stash_backward(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tensor], dh: Sequence[torch.Tensor],
+                   handle: Optional[Handle] = None, stream=None):
+    """(du, h): GeLU's gradient du[k] = dh[k] GeLU'(u) and its value h[k] =
+    GeLU(u), u the 8-bit activations of `stash_pack`."""
+    dev, p, M, F = _check_stash(codes, scales)
+    _check_shards("dh", dh, p)
+    _check("dh", dh, (M, F), device=dev)
+    with _on(stream):
+        du = [torch.empty((M, F), dtype=torch.bfloat16, device=dev) for _ in range(p)]
+        h = [torch.empty((M, F), dtype=torch.bfloat16, device=dev) for _ in range(p)]
+    hd = _handle(handle, dev, stream)
+    check(load().tpf_stash_backward(hd.ptr, p, M, F, _ptrs(codes), _ptrs(scales), _ptrs(dh), _ptrs(du), _ptrs(h),
+                                    _stream_ptr(stream)))
+    return du, h
+
+
+def stash_weight_grad(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tensor], dY: Sequence[torch.Tensor],
+                      out_dtype=torch.float32, dW=None, ws: Optional[torch.Tensor] = None,
+                      handle: Optional[Handle] = None, stream=None) -> List[torch.Tensor]:
+    """dW[k] = U_k^T dY[k], U_k [M, R] the 8-bit activations of `stash_pack`:
+    `weight_grad` of an input kept in 8 bits."""
+    dev, p, M, R = _check_stash(codes, scales)
+    _check_shards("dY", dY, p)
+    C = dY[0].shape[1]
+    _check("dY", dY, (M, C), device=dev)
+    if dW is None:
+        with _on(stream):
+            dW = [torch.empty((R, C), dtype=out_dtype, device=dev) for _ in range(p)]
+    _check_shards("dW", dW, p)
+    _check("dW", dW, (R, C), OUT_DTYPES, dev)
+    _need(all(d.dtype == dW[0].dtype for d in dW), "dW: the shards differ in dtype")
+    _check_ws(ws, dev)
+    need = load().tpf_stash_weight_grad_ws(p, M, R, C)
+    if ws is None and need:
+        with _on(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    hd = _handle(handle, dev, stream)
+    check(load().tpf_stash_weight_grad(hd.ptr, p, M, R, C, _ptrs(codes), _ptrs(scales), _ptrs(dY), _ptrs(dW),
+                                       _dtype_code(dW[0].dtype), ws.data_ptr() if ws is not None else None,
+                                       ws.numel() * ws.element_size() if ws is not None else 0, _stream_ptr(stream)))
+    return dW
+
+
+def qweight_matmul(X: Sequence[torch.Tensor], codes: Sequence[torch.Tensor], scales: Sequence[torch.Tensor],
+                   zeros: Optional[Sequence[torch.Tensor]] = None, group: int = 128, gelu: bool = False,
+                   out_dtype=torch.bfloat16, Y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                   handle: Optional[Handle] = None, stream=None) -> torch.Tensor:
+    """Y = sum_k X[k] W_k^T with 4-bit weights (row-parallel over the shards;
+    p = 1: any Linear), GeLU of it with `gelu`.
+
+    X[k] [M, K] bf16; codes[k] [N, K/2] uint8, byte j of every four holding
+    code j (low half) and code j + 4 (high half) of a run of eight; scales[k]
+    [N, K/group] bf16; zeros[k] [N, K/group] uint8 (None: 8).
+    W_k = (code - zero) * scale; group is 32, 64 or 128."""
+    p = len(X)
+    _need(p >= 1, "X: no shards given")
+    _need(X[0].dim() == 2, f"X[0] has {X[0].dim()} dimensions, expected [M, K]")
+    M, K = X[0].shape
+    _need(group in (32, 64, 128) and K % group == 0, f"group {group} is not 32, 64 or 128 or does not divide K = {K}")
+    _check_shards("codes", codes, p)
+    _check_shards("scales", scales, p)
+    dev = _check("X", X, (M, K))
+    N = codes[0].shape[0]
+    _check("codes", codes, (N, K // 2), (torch.uint8,), dev)
+    _check("scales", scales, (N, K // group), (torch.bfloat16,), dev)
+    if zeros is not None:
+        _check_shards("zeros", zeros, p)
+        _check("zeros", zeros, (N, K // group), (torch.uint8,), dev)
+    if Y is None:
+        with _on(stream):
+            Y = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _check("Y", [Y], (M, N), OUT_DTYPES, dev)
+    _check_ws(ws, dev)
+    need = load().tpf_qweight_matmul_ws(p, M, K, N, group)
+    if ws is None and need:
+        with _on(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    hd = _handle(handle, dev, stream)
+    check(load().tpf_qweight_matmul(hd.ptr, p, M, K, N, group, _ptrs(X), _ptrs(codes), _ptrs(scales),
+                                    _ptrs(zeros) if zeros is not None else None, 1 if gelu else 0, Y.data_ptr(),
+                                    _dtype_code(Y.dtype), ws.data_ptr() if ws is not None else None,
+                                    ws.numel() * ws.element_size() if ws is not None else 0, _stream_ptr(stream)))
+    return Y
