@@ -16,9 +16,10 @@ CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libtpfuse.so")
 
-SOURCES = ["tpf_kernels.hip", "tpf_api.cpp", "tpf_block_api.cpp", "tpf_norm.hip", "tpf_stash.hip", "tpf_qweight.hip"]
+SOURCES = ["tpf_kernels.hip", "tpf_api.cpp", "tpf_block_api.cpp", "tpf_norm.hip", "tpf_stash.hip",
+           "tpf_stash_grad.hip", "tpf_qweight.hip"]
 HEADERS = ["tpf_device.hpp", "tpf_internal.hpp", "tpf_gemm.hpp", "tpf_stationary.hpp", "tpf_host.hpp",
-           "tpf_block.hpp"]
+           "tpf_block.hpp", "tpf_tiles.hpp"]
 
 # Packed-fp32 instructions are disabled for all device code: the compiler
 # would otherwise form v_pk_* fp32 ops from plain float code.

@@ -71,8 +71,12 @@ struct StashGradArgs {
   void* dW[kMaxShards];              // [R][C]
   int p, M, R, C;
   int out;                           // OUT_F32 or OUT_BF16
+  float* partial;                    // splits > 1: [splits][p][R][C]
+  int splits, steps;                 // the contraction's K steps, and the parts they are cut into
   int tiles_m, tiles_n, tasks;
 };
+// Parts that the contraction is cut into for these sizes (1: no workspace).
+int stash_grad_splits(int p, int64_t M, int64_t R, int64_t C);
 hipError_t launch_stash_weight_grad(StashGradArgs a, hipStream_t s);
 
 // ---------------------------------------------------------------------------
@@ -87,7 +91,11 @@ struct QweightArgs {
   void* Y;                           // [M][N]
   int p, M, K, N, group;
   int gelu, out;
+  float* partial;                    // splits > 1: [splits][M][N]
+  int splits;
 };
+// Parts that the contraction is cut into for these sizes (1: no workspace).
+int qweight_splits(int p, int64_t M, int64_t K, int64_t N);
 hipError_t launch_qweight(const QweightArgs& a, hipStream_t s);
 
 }  // namespace tpf

@@ -26,6 +26,19 @@ int guarded(F f) {
   }
 }
 
+// A size query: leaves the last error alone.
+template <class F>
+size_t guarded_size(F f) {
+  try {
+    const std::string saved = g_last_error;
+    const size_t n = f();
+    g_last_error = saved;
+    return n;
+  } catch (...) {
+    return 0;
+  }
+}
+
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 int check_ptrs_at(const void* const* arr, int count, const char* name, uintptr_t n) {
@@ -263,8 +276,11 @@ int tpf_stash_backward(tpf_handle h, int p, int64_t M, int64_t F, const void* co
 }
 
 size_t tpf_stash_weight_grad_ws(int p, int64_t M, int64_t R, int64_t C) {
-  (void)p, (void)M, (void)R, (void)C;
-  return 0;
+  return guarded_size([&]() -> size_t {
+    if (check_stash_grad(p, M, R, C) != TPF_OK) return 0;
+    const int splits = stash_grad_splits(p, M, R, C);
+    return splits > 1 ? (size_t)splits * p * R * C * sizeof(float) : 0;
+  });
 }
 
 int tpf_stash_weight_grad(tpf_handle h, int p, int64_t M, int64_t R, int64_t C, const void* const* codes,
@@ -293,6 +309,8 @@ int tpf_stash_weight_grad(tpf_handle h, int p, int64_t M, int64_t R, int64_t C, 
     a.R = (int)R;
     a.C = (int)C;
     a.out = out_kind(dw_dtype);
+    a.partial = reinterpret_cast<float*>(ws);
+    a.splits = stash_grad_splits(p, M, R, C);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     TPF_TIMED(h, s, launch_stash_weight_grad(a, s));
     return TPF_OK;
@@ -300,8 +318,11 @@ int tpf_stash_weight_grad(tpf_handle h, int p, int64_t M, int64_t R, int64_t C, 
 }
 
 size_t tpf_qweight_matmul_ws(int p, int64_t M, int64_t K, int64_t N, int group) {
-  (void)p, (void)M, (void)K, (void)N, (void)group;
-  return 0;
+  return guarded_size([&]() -> size_t {
+    if (check_qweight(p, M, K, N, group) != TPF_OK) return 0;
+    const int splits = qweight_splits(p, M, K, N);
+    return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0;
+  });
 }
 
 int tpf_qweight_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, int group, const void* const* X,
@@ -334,6 +355,8 @@ int tpf_qweight_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, int
     a.group = group;
     a.gelu = gelu;
     a.out = out_kind(y_dtype);
+    a.partial = reinterpret_cast<float*>(ws);
+    a.splits = qweight_splits(p, M, K, N);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     TPF_TIMED(h, s, launch_qweight(a, s));
     return TPF_OK;

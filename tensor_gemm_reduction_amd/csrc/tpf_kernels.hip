@@ -25,6 +25,7 @@
 
 #include "tpf_internal.hpp"
 #include "tpf_stationary.hpp"
+#include "tpf_tiles.hpp"
 
 // The launchers are split into parts so that the build can compile them as
 // separate translation units in parallel (-DTPF_PART=n, n = 0..8); without
@@ -91,25 +92,6 @@ __device__ __forceinline__ TileJob make_job(const GemmOperands& g, int shard, in
   j.N = g.N;
   j.K = g.K;
   return j;
-}
-
-// Tile u of a row range (shard-major) -> (shard, tm, tn).  Within a shard the
-// tiles go in groups of kGroupM tile-rows, column by column, so that tiles
-// running at the same time share A and B panels (the 32 tiles an XCD runs
-// at once cover 8 row panels x 4 column panels; measured about 1 % faster
-// than groups of 4 rows, groups of 2 or 16 slower).
-constexpr int kGroupM = 8;
-
-__device__ __forceinline__ void tile_coords(int u, int tiles_m, int tiles_n, int& shard, int& tm, int& tn) {
-  const int per_shard = tiles_m * tiles_n;
-  shard = u / per_shard;
-  const int t = u - shard * per_shard;
-  const int group = t / (kGroupM * tiles_n);
-  const int first = group * kGroupM;
-  const int gsize = min(kGroupM, tiles_m - first);
-  const int w = t - first * tiles_n;
-  tm = first + w % gsize;
-  tn = w / gsize;
 }
 
 template <int OUT, int PB>
@@ -359,15 +341,6 @@ __global__ __launch_bounds__(Cfg::THREADS) void fused_kernel(FusedArgs args) {
       atomic_store_relaxed(&ctl->done, 0);
     }
   }
-}
-
-// Block b of a grid of `total` blocks -> task index.  Blocks are dealt to the
-// XCDs round-robin (block b runs on XCD b % 8), so the tasks are split into
-// kXcds contiguous shares and block b takes task b / 8 of share b % 8: each
-// XCD's L2 then sees a contiguous run of tiles.
-__device__ __forceinline__ int xcd_task(int b, int total) {
-  const int x = b & (kXcds - 1), i = b / kXcds;
-  return x * (total / kXcds) + min(x, total % kXcds) + i;
 }
 
 // Sum output tile (m0, rows, n0, ncols) over the p shards' partials.

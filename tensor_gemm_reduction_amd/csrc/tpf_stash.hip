@@ -1,5 +1,5 @@
 // Activations kept in 8 bits for the backward pass: pack (with the forward's
-// GeLU), GeLU's gradient and the weight gradient that read them.
+// GeLU) and GeLU's gradient from them.
 //
 // A block of 32 x 32 values shares the least power of two s >= 2^-117 with
 // max|finite u| <= 448 s; codes are e4m3(u / s), round to nearest even, and
@@ -164,64 +164,6 @@ hipError_t launch_stash_backward(const StashArgs& a, int num_cus, hipStream_t s)
   const int64_t groups = ((int64_t)a.M * (a.F / 8) + 255) / 256;
   const int64_t cap = std::max<int64_t>(1, (int64_t)num_cus * 32 / a.p);
   hipLaunchKernelGGL(stash_backward_kernel, dim3((unsigned)std::min(groups, cap), (unsigned)a.p), dim3(256), 0, s, a);
-  return hipGetLastError();
-}
-
-// dW_k = U_k^T dY_k, U = code * scale.  64 x 64 output tiles of four waves,
-// each a 32 x 32 block; 16 rows of the contraction a step through LDS,
-// transposed as they are written.
-constexpr int kSgTile = 64;
-__global__ __launch_bounds__(256) void stash_grad_kernel(StashGradArgs args) {
-  (void)args;
-  const StashGradArgs& a = stash_kernarg<StashGradArgs>();
-  __shared__ __bf16 ua[kSgTile][24], yb[kSgTile][24];   // [column][row of the step], padded
-  const int per = a.tiles_m * a.tiles_n;
-  const int k = blockIdx.x / per, t = blockIdx.x % per;
-  const int r0 = (t / a.tiles_n) * kSgTile, c0 = (t % a.tiles_n) * kSgTile;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wr = (wave >> 1) * 32, wc = (wave & 1) * 32;
-  const int nsc = (a.R + 31) / 32;
-  const int col = threadIdx.x & 63, rs = threadIdx.x >> 6;    // loader: one column, rows rs + 4 i
-  f32x16_t acc;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  for (int m0 = 0; m0 < a.M; m0 += 16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = m0 + rs + 4 * i;
-      __bf16 u = (__bf16)0.0f, y = (__bf16)0.0f;
-      if (row < a.M && r0 + col < a.R) {
-        const float scale =
-            __uint_as_float((uint32_t)a.scales[k][(int64_t)(row >> 5) * nsc + ((r0 + col) >> 5)] << 23);
-        u = (__bf16)(__builtin_amdgcn_cvt_f32_fp8((int)a.codes[k][(int64_t)row * a.R + r0 + col], 0) * scale);
-      }
-      if (row < a.M && c0 + col < a.C) y = a.dY[k][(int64_t)row * a.C + c0 + col];
-      ua[col][rs + 4 * i] = u;
-      yb[col][rs + 4 * i] = y;
-    }
-    __syncthreads();
-    const bf16x8_t av = *reinterpret_cast<const bf16x8_t*>(&ua[wr + (lane & 31)][(lane >> 5) * 8]);
-    const bf16x8_t bv = *reinterpret_cast<const bf16x8_t*>(&yb[wc + (lane & 31)][(lane >> 5) * 8]);
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, bv, acc, 0, 0, 0);
-    __syncthreads();
-  }
-  const int c = c0 + wc + (lane & 31);
-#pragma unroll
-  for (int v = 0; v < 16; ++v) {
-    const int r = r0 + wr + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-    if (r < a.R && c < a.C) {
-      const int64_t at = (int64_t)r * a.C + c;
-      if (a.out == OUT_F32) reinterpret_cast<float*>(a.dW[k])[at] = acc[v];
-      else reinterpret_cast<__bf16*>(a.dW[k])[at] = (__bf16)acc[v];
-    }
-  }
-}
-
-hipError_t launch_stash_weight_grad(StashGradArgs a, hipStream_t s) {
-  a.tiles_m = (a.R + kSgTile - 1) / kSgTile;
-  a.tiles_n = (a.C + kSgTile - 1) / kSgTile;
-  a.tasks = a.p * a.tiles_m * a.tiles_n;
-  hipLaunchKernelGGL(stash_grad_kernel, dim3((unsigned)a.tasks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

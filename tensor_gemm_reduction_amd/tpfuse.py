@@ -547,7 +547,37 @@ CODE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
 def _ptrs(ts):
-    return ptr_array([t.data_ptr() for t in ts])
+    return (_VP * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def _all_ok(ts, idx: int, dtype, shape) -> bool:
+    """Whether every tensor is on GPU `idx`, contiguous, of one dtype and shape.
+
+    Decode-sized calls run for a few microseconds on the GPU, so the checks of
+    good arguments are this one pass; `_check` names what is wrong."""
+    for t in ts:
+        if t.get_device() != idx or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+            return False
+    return True
+
+
+def _ctx(handle: Optional[Handle], dev, stream):
+    """(handle, raw stream) of a call; the current stream is asked for once."""
+    idx = dev.index
+    sp = torch._C._cuda_getCurrentRawStream(idx) if stream is None else int(stream.cuda_stream)
+    h = handle or _default_handles.get((idx, sp)) or default_handle(idx, stream)
+    _need(h.device == idx, f"handle is bound to device {h.device}, tensors are on {dev}")
+    return h._h, sp
+
+
+def _shards(p: int, shape, dtype, dev):
+    """p new tensors of one shape, from one allocation while that keeps them aligned."""
+    size = dtype.itemsize
+    for n in shape:
+        size *= n
+    if size % 16 == 0 or dtype is torch.uint8:
+        return torch.empty((p, *shape), dtype=dtype, device=dev).unbind(0)
+    return [torch.empty(shape, dtype=dtype, device=dev) for _ in range(p)]
 
 
 def _norm_operands(x, blocks, w_pre, w_post, gate):
@@ -556,14 +586,20 @@ def _norm_operands(x, blocks, w_pre, w_post, gate):
     _need(p >= 1, "blocks: no tensors given")
     _need(x.dim() == 2, f"x has {x.dim()} dimensions, expected [M, H]")
     M, H = x.shape
-    dev = _check("x", [x], (M, H), OUT_DTYPES)
+    dev, idx = x.device, x.get_device()
+    kind = GATE_NONE if gate is None else GATE_TOKEN if gate.dim() == 2 else GATE_CHANNEL
+    vec = (H,)
+    if (idx >= 0 and x.dtype in OUT_DTYPES and x.is_contiguous() and blocks[0].dtype in OUT_DTYPES
+            and _all_ok(blocks, idx, blocks[0].dtype, x.shape) and w_pre.dtype in OUT_DTYPES
+            and _all_ok((w_pre, w_post), idx, w_pre.dtype, vec)
+            and (gate is None or _all_ok((gate,), idx, w_pre.dtype, (M, 1) if kind == GATE_TOKEN else vec))):
+        return dev, M, H, kind
+    _check("x", [x], (M, H), OUT_DTYPES)
     _check("blocks", blocks, (M, H), OUT_DTYPES, dev)
     _need(all(b.dtype == blocks[0].dtype for b in blocks), "blocks: the tensors differ in dtype")
     _check("w_pre", [w_pre], (H,), OUT_DTYPES, dev)
     _check("w_post", [w_post], (H,), (w_pre.dtype,), dev)
-    kind = GATE_NONE
     if gate is not None:
-        kind = GATE_TOKEN if gate.dim() == 2 else GATE_CHANNEL
         _check("gate", [gate], (M, 1) if kind == GATE_TOKEN else (H,), (w_pre.dtype,), dev)
     return dev, M, H, kind
 
@@ -583,20 +619,22 @@ def block_norm(x: torch.Tensor, blocks: Sequence[torch.Tensor], w_pre: torch.Ten
     are stored as offsets from 1 with `unit_offset`.  `stats` ([2, M] fp32, for
     `block_norm_backward`) is None unless `want_stats`."""
     dev, M, H, kind = _norm_operands(x, blocks, w_pre, w_post, gate)
+    if x_out is not None:
+        _check("x_out", [x_out], (M, H), (x.dtype,), dev)
+    if y is not None:
+        _check("y", [y], (M, H), (torch.bfloat16,), dev)
     with _on(stream):
         if x_out is None:
             x_out = torch.empty_like(x)
         if y is None:
-            y = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+            y = torch.empty_like(x, dtype=torch.bfloat16)
         stats = torch.empty((2, M), dtype=torch.float32, device=dev) if want_stats else None
-    _check("x_out", [x_out], (M, H), (x.dtype,), dev)
-    _check("y", [y], (M, H), (torch.bfloat16,), dev)
-    h = _handle(handle, dev, stream)
-    check(load().tpf_block_norm(h.ptr, len(blocks), M, H, x.data_ptr(), _dtype_code(x.dtype), _ptrs(blocks),
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_block_norm(h, len(blocks), M, H, x.data_ptr(), _dtype_code(x.dtype), _ptrs(blocks),
                                 _dtype_code(blocks[0].dtype), w_pre.data_ptr(), w_post.data_ptr(),
                                 gate.data_ptr() if gate is not None else None, kind, _dtype_code(w_pre.dtype), alpha,
                                 beta, eps, 1 if unit_offset else 0, x_out.data_ptr(), y.data_ptr(),
-                                stats.data_ptr() if stats is not None else None, _stream_ptr(stream)))
+                                stats.data_ptr() if stats is not None else None, sp))
     return x_out, y, stats
 
 
@@ -625,14 +663,14 @@ def block_norm_backward(dy: torch.Tensor, dx_out: Optional[torch.Tensor], x: tor
         dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev) if gate is not None else None
         if ws is None:
             ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    h = _handle(handle, dev, stream)
+    h, sp = _ctx(handle, dev, stream)
     check(load().tpf_block_norm_backward(
-        h.ptr, len(blocks), M, H, dy.data_ptr(), dx_out.data_ptr() if dx_out is not None else None, x.data_ptr(),
+        h, len(blocks), M, H, dy.data_ptr(), dx_out.data_ptr() if dx_out is not None else None, x.data_ptr(),
         _dtype_code(x.dtype), _ptrs(blocks), _dtype_code(blocks[0].dtype), stats.data_ptr(), w_pre.data_ptr(),
         w_post.data_ptr(), gate.data_ptr() if gate is not None else None, kind, _dtype_code(w_pre.dtype), alpha, beta,
         1 if unit_offset else 0, dx.data_ptr(), db.data_ptr(), dw_pre.data_ptr(), dw_post.data_ptr(),
         dgate.data_ptr() if dgate is not None else None, ws.data_ptr(), ws.numel() * ws.element_size(),
-        _stream_ptr(stream)))
+        sp))
     return dx, db, dw_pre, dw_post, dgate
 
 
@@ -650,14 +688,16 @@ def stash_pack(u: Sequence[torch.Tensor], gelu: bool = True, handle: Optional[Ha
     _need(p >= 1, "u: no shards given")
     _need(u[0].dim() == 2, f"u[0] has {u[0].dim()} dimensions, expected [M, F]")
     M, F = u[0].shape
-    dev = _check("u", u, (M, F))
+    dev = u[0].device
+    if not (u[0].is_cuda and _all_ok(u, u[0].get_device(), torch.bfloat16, (M, F))):
+        _check("u", u, (M, F))
     with _on(stream):
-        codes = [torch.empty((M, F), dtype=torch.float8_e4m3fn, device=dev) for _ in range(p)]
-        scales = [torch.empty(_stash_shape(M, F), dtype=torch.uint8, device=dev) for _ in range(p)]
-        h = [torch.empty((M, F), dtype=torch.bfloat16, device=dev) for _ in range(p)] if gelu else None
-    hd = _handle(handle, dev, stream)
-    check(load().tpf_stash_pack(hd.ptr, p, M, F, _ptrs(u), 1 if gelu else 0, _ptrs(h) if gelu else None,
-                                _ptrs(codes), _ptrs(scales), _stream_ptr(stream)))
+        codes = _shards(p, (M, F), torch.float8_e4m3fn, dev)
+        scales = _shards(p, _stash_shape(M, F), torch.uint8, dev)
+        h = _shards(p, (M, F), torch.bfloat16, dev) if gelu else None
+    hd, sp = _ctx(handle, dev, stream)
+    check(load().tpf_stash_pack(hd, p, M, F, _ptrs(u), 1 if gelu else 0, _ptrs(h) if gelu else None,
+                                _ptrs(codes), _ptrs(scales), sp))
     return h, codes, scales
 
 
@@ -667,8 +707,11 @@ def _check_stash(codes, scales):
     _need(codes[0].dim() == 2, f"codes[0] has {codes[0].dim()} dimensions, expected [M, F]")
     M, F = codes[0].shape
     _check_shards("scales", scales, p)
-    dev = _check("codes", codes, (M, F), CODE_DTYPES)
-    _check("scales", scales, _stash_shape(M, F), (torch.uint8,), dev)
+    dev, idx = codes[0].device, codes[0].get_device()
+    if not (idx >= 0 and codes[0].dtype in CODE_DTYPES and _all_ok(codes, idx, codes[0].dtype, (M, F))
+            and _all_ok(scales, idx, torch.uint8, _stash_shape(M, F))):
+        _check("codes", codes, (M, F), CODE_DTYPES)
+        _check("scales", scales, _stash_shape(M, F), (torch.uint8,), dev)
     return dev, p, M, F
 
 
@@ -678,13 +721,13 @@ def stash_backward(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tensor]
     GeLU(u), u the 8-bit activations of `stash_pack`."""
     dev, p, M, F = _check_stash(codes, scales)
     _check_shards("dh", dh, p)
-    _check("dh", dh, (M, F), device=dev)
+    if not _all_ok(dh, dev.index, torch.bfloat16, (M, F)):
+        _check("dh", dh, (M, F), device=dev)
     with _on(stream):
-        du = [torch.empty((M, F), dtype=torch.bfloat16, device=dev) for _ in range(p)]
-        h = [torch.empty((M, F), dtype=torch.bfloat16, device=dev) for _ in range(p)]
-    hd = _handle(handle, dev, stream)
-    check(load().tpf_stash_backward(hd.ptr, p, M, F, _ptrs(codes), _ptrs(scales), _ptrs(dh), _ptrs(du), _ptrs(h),
-                                    _stream_ptr(stream)))
+        du, h = _shards(p, (M, F), torch.bfloat16, dev), _shards(p, (M, F), torch.bfloat16, dev)
+    hd, sp = _ctx(handle, dev, stream)
+    check(load().tpf_stash_backward(hd, p, M, F, _ptrs(codes), _ptrs(scales), _ptrs(dh), _ptrs(du), _ptrs(h),
+                                    sp))
     return du, h
 
 
@@ -708,10 +751,10 @@ def stash_weight_grad(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tens
     if ws is None and need:
         with _on(stream):
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    hd = _handle(handle, dev, stream)
-    check(load().tpf_stash_weight_grad(hd.ptr, p, M, R, C, _ptrs(codes), _ptrs(scales), _ptrs(dY), _ptrs(dW),
+    hd, sp = _ctx(handle, dev, stream)
+    check(load().tpf_stash_weight_grad(hd, p, M, R, C, _ptrs(codes), _ptrs(scales), _ptrs(dY), _ptrs(dW),
                                        _dtype_code(dW[0].dtype), ws.data_ptr() if ws is not None else None,
-                                       ws.numel() * ws.element_size() if ws is not None else 0, _stream_ptr(stream)))
+                                       ws.numel() * ws.element_size() if ws is not None else 0, sp))
     return dW
 
 
@@ -733,25 +776,32 @@ def qweight_matmul(X: Sequence[torch.Tensor], codes: Sequence[torch.Tensor], sca
     _need(group in (32, 64, 128) and K % group == 0, f"group {group} is not 32, 64 or 128 or does not divide K = {K}")
     _check_shards("codes", codes, p)
     _check_shards("scales", scales, p)
-    dev = _check("X", X, (M, K))
-    N = codes[0].shape[0]
-    _check("codes", codes, (N, K // 2), (torch.uint8,), dev)
-    _check("scales", scales, (N, K // group), (torch.bfloat16,), dev)
     if zeros is not None:
         _check_shards("zeros", zeros, p)
-        _check("zeros", zeros, (N, K // group), (torch.uint8,), dev)
+    N, per_group = codes[0].shape[0], (codes[0].shape[0], K // group)
+    dev, idx = X[0].device, X[0].get_device()
+    if not (idx >= 0 and _all_ok(X, idx, torch.bfloat16, (M, K)) and _all_ok(codes, idx, torch.uint8, (N, K // 2))
+            and _all_ok(scales, idx, torch.bfloat16, per_group)
+            and (zeros is None or _all_ok(zeros, idx, torch.uint8, per_group))):
+        _check("X", X, (M, K))
+        _check("codes", codes, (N, K // 2), (torch.uint8,), dev)
+        _check("scales", scales, per_group, (torch.bfloat16,), dev)
+        if zeros is not None:
+            _check("zeros", zeros, per_group, (torch.uint8,), dev)
     if Y is None:
+        _need(out_dtype in OUT_DTYPES, f"output dtype must be bfloat16 or float32, got {out_dtype}")
         with _on(stream):
             Y = torch.empty((M, N), dtype=out_dtype, device=dev)
-    _check("Y", [Y], (M, N), OUT_DTYPES, dev)
+    else:
+        _check("Y", [Y], (M, N), OUT_DTYPES, dev)
     _check_ws(ws, dev)
     need = load().tpf_qweight_matmul_ws(p, M, K, N, group)
     if ws is None and need:
         with _on(stream):
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    hd = _handle(handle, dev, stream)
-    check(load().tpf_qweight_matmul(hd.ptr, p, M, K, N, group, _ptrs(X), _ptrs(codes), _ptrs(scales),
+    hd, sp = _ctx(handle, dev, stream)
+    check(load().tpf_qweight_matmul(hd, p, M, K, N, group, _ptrs(X), _ptrs(codes), _ptrs(scales),
                                     _ptrs(zeros) if zeros is not None else None, 1 if gelu else 0, Y.data_ptr(),
                                     _dtype_code(Y.dtype), ws.data_ptr() if ws is not None else None,
-                                    ws.numel() * ws.element_size() if ws is not None else 0, _stream_ptr(stream)))
+                                    ws.numel() * ws.element_size() if ws is not None else 0, sp))
     return Y
