@@ -19,38 +19,48 @@ struct F8 {
   float v[8];
 };
 
-// Eight consecutive elements at element e (16-byte aligned), widened exactly.
+// Eight consecutive elements as loaded, and widened exactly.
 template <int F32>
-__device__ __forceinline__ F8 load8(const void* base, int64_t e) {
+struct Raw8 {
+  u32x4_t w[F32 ? 2 : 1];
+};
+template <int F32>
+__device__ __forceinline__ Raw8<F32> load_raw(const void* base, int64_t e) {
+  Raw8<F32> r;
+  const u32x4_t* q = reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(base) + e * (F32 ? 4 : 2));
+  r.w[0] = q[0];
+  if constexpr (F32) r.w[1] = q[1];
+  return r;
+}
+template <int F32>
+__device__ __forceinline__ F8 widen(const Raw8<F32>& r) {
   F8 o;
   if constexpr (F32) {
-    const f32x4_t* q = reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(base) + e);
-    const f32x4_t a = q[0], b = q[1];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      o.v[i] = a[i];
-      o.v[i + 4] = b[i];
+      o.v[i] = __uint_as_float(r.w[0][i]);
+      o.v[i + 4] = __uint_as_float(r.w[1][i]);
     }
   } else {
-    const u32x4_t w = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint16_t*>(base) + e);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      o.v[2 * i] = __uint_as_float(w[i] << 16);
-      o.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      o.v[2 * i] = __uint_as_float(r.w[0][i] << 16);
+      o.v[2 * i + 1] = __uint_as_float(r.w[0][i] & 0xffff0000u);
     }
   }
   return o;
+}
+template <int F32>
+__device__ __forceinline__ F8 load8(const void* base, int64_t e) {
+  return widen<F32>(load_raw<F32>(base, e));
 }
 
 __device__ __forceinline__ F8 load8_any(const void* base, int64_t e, int f32) {
   return f32 ? load8<1>(base, e) : load8<0>(base, e);
 }
-
-__device__ __forceinline__ u32x4_t to_bf16x8(const F8& x) {
-  bf16x8_t h;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = (__bf16)x.v[i];
-  return __builtin_bit_cast(u32x4_t, h);
+__device__ __forceinline__ float load1_any(const void* base, int64_t e, int f32) {
+  return f32 ? reinterpret_cast<const float*>(base)[e]
+             : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[e] << 16);
 }
 
 template <int F32>
@@ -60,52 +70,51 @@ __device__ __forceinline__ void store8(void* base, int64_t e, const F8& x) {
     q[0] = f32x4_t{x.v[0], x.v[1], x.v[2], x.v[3]};
     q[1] = f32x4_t{x.v[4], x.v[5], x.v[6], x.v[7]};
   } else {
-    *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(base) + e) = to_bf16x8(x);
+    bf16x8_t h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (__bf16)x.v[i];
+    *reinterpret_cast<bf16x8_t*>(reinterpret_cast<uint16_t*>(base) + e) = h;
   }
 }
 
-// The left fold over the p shards of eight elements, loads four at a time.
+// Adds shards 1 .. p-1 to s in order, loads three at a time.
 template <int F32>
-__device__ __forceinline__ F8 load_sum8(const NormArgs& a, int64_t e) {
-  F8 s = load8<F32>(a.blocks[0], e);
+__device__ __forceinline__ void add_shards(F8& s, const NormArgs& a, int64_t e) {
   for (int k = 1; k < a.p; k += 3) {
-    F8 t[3];
+    Raw8<F32> t[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j)
-      if (k + j < a.p) t[j] = load8<F32>(a.blocks[k + j], e);
+      if (k + j < a.p) t[j] = load_raw<F32>(a.blocks[k + j], e);
 #pragma unroll
     for (int j = 0; j < 3; ++j)
       if (k + j < a.p) {
+        const F8 f = widen<F32>(t[j]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s.v[i] += t[j].v[i];
+        for (int i = 0; i < 8; ++i) s.v[i] += f.v[i];
       }
   }
-  return s;
 }
 
-// Sums of N values over a row's T threads; every thread gets them, added in
-// the same order whatever the number of rows.
-template <int T, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* lds) {
+// Sums of N values over the waves of a row (at most 16); every thread gets
+// them, added in an order that depends on the row's length alone.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[16], int waves, int wave) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d);
-  if constexpr (T > 64) {
-    constexpr int W = T / 64;
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
+  if (waves == 1) return;
+  const int lane = threadIdx.x & 63;
+  if (lane == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) lds[i * W + wave] = v[i];
-    }
-    __syncthreads();
+    for (int i = 0; i < N; ++i) lds[i][wave] = v[i];
+  }
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = 0.0f;
+  for (int i = 0; i < N; ++i) {
+    v[i] = (lane & 15) < waves ? lds[i][lane & 15] : 0.0f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) s += lds[i * W + w];
-      v[i] = s;
-    }
+    for (int d = 8; d >= 1; d >>= 1) v[i] += __shfl_xor(v[i], d);
   }
 }
 
@@ -114,50 +123,55 @@ __device__ __forceinline__ const A& norm_kernarg() {
   return *(const A*)__builtin_amdgcn_kernarg_segment_ptr();
 }
 
-// T threads a row, V vectors of eight elements a thread; workgroups of at
-// least 256 threads, so short rows share one.
-template <int T>
-constexpr int norm_rows() {
-  return T < 256 ? (T == 64 ? 4 : 1) : 1;
+// A row takes the fewest whole waves that hold it at V vectors of eight
+// elements a thread (odd widths leave at most a wave's worth idle); rows of
+// one wave share workgroups of four.
+constexpr int kNormRows = 4;
+template <int V>
+static int norm_threads(int H) {
+  return (H + 512 * V - 1) / (512 * V) * 64;
 }
 
-template <int XF, int BF, int T, int V>
-__global__ __launch_bounds__(T * norm_rows<T>()) void block_norm_kernel(NormArgs args) {
+template <int XF, int BF, int V>
+__global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs args) {
   (void)args;
   const NormArgs& a = norm_kernarg<NormArgs>();
-  __shared__ float lds[2][T / 64];
-  const int t = threadIdx.x % T;
-  const int m = blockIdx.x * norm_rows<T>() + threadIdx.x / T;
-  if (norm_rows<T>() > 1 && m >= a.M) return;
+  __shared__ float lds[2][1][16];
+  const int T = blockDim.x, t = threadIdx.x, waves = T / 64, wave = t >> 6;
+  const int m = blockIdx.x * blockDim.y + threadIdx.y;
+  if (m >= a.M) return;      // only where a row is one wave: no barrier follows
   const int64_t row = (int64_t)m * a.H;
-  F8 b[V], x[V];
+  F8 b[V];
+  Raw8<XF> xr[V];
   float s[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int h = (i * T + t) * 8;
     if (h < a.H) {
-      b[i] = load_sum8<BF>(a, row + h);
-      x[i] = load8<XF>(a.x, row + h);
+      b[i] = load8<BF>(a.blocks[0], row + h);
+      xr[i] = load_raw<XF>(a.x, row + h);
     }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if ((i * T + t) * 8 < a.H) {
+  for (int i = 0; i < V; ++i) {
+    const int h = (i * T + t) * 8;
+    if (h < a.H) {
+      add_shards<BF>(b[i], a, row + h);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[0] += b[i].v[j] * b[i].v[j];
     }
-  row_sums<T, 1>(s, lds[0]);
+  }
+  row_sums<1>(s, lds[0], waves, wave);
   const float inv_h = 1.0f / (float)a.H;
   const float rb = 1.0f / sqrtf(s[0] * inv_h + a.eps);
-  const float g_row = a.gate_kind == GATE_TOKEN ? (a.w_f32 ? reinterpret_cast<const float*>(a.gate)[m]
-                                                           : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.gate)[m] << 16))
-                                                : 1.0f;
-  const float scale = a.beta * g_row;
+  const float scale = a.gate_kind == GATE_TOKEN ? a.beta * load1_any(a.gate, m, a.w_f32) : a.beta;
+  F8 x[V];
   s[0] = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int h = (i * T + t) * 8;
     if (h < a.H) {
+      x[i] = widen<XF>(xr[i]);
       const F8 w = load8_any(a.w_post, h, a.w_f32);
       F8 g;
       if (a.gate_kind == GATE_CHANNEL) g = load8_any(a.gate, h, a.w_f32);
@@ -173,7 +187,7 @@ __global__ __launch_bounds__(T * norm_rows<T>()) void block_norm_kernel(NormArgs
       store8<XF>(a.x_out, row + h, x[i]);
     }
   }
-  row_sums<T, 1>(s, lds[1]);
+  row_sums<1>(s, lds[1], waves, wave);
   const float rx = 1.0f / sqrtf(s[0] * inv_h + a.eps);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -205,89 +219,135 @@ __global__ __launch_bounds__(T * norm_rows<T>()) void block_norm_kernel(NormArgs
 // gate gradient is Q (w_post + o), so two sums serve three gradients.
 // Workgroup i adds rows i, i + groups, ... in registers; norm_columns_kernel
 // adds the workgroups in a fixed order.
-template <int XF, int BF, int T, int V>
-__global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs args) {
+// With V = 1 (rows of up to 8192) a thread loads the next row before it joins
+// the current one, so that the row's barrier does not leave the memory idle,
+// and keeps its columns' bf16 weights and gate.  16 waves leave 128 registers a
+// thread: longer rows are read again from the cache after the sums instead of
+// being held, and so are fp32 weights.
+template <int XF, int BF, int WF, int V>
+__global__ __launch_bounds__(1024) void block_norm_backward_kernel(NormArgs args) {
   (void)args;
   const NormArgs& a = norm_kernarg<NormArgs>();
-  __shared__ float lds[2][3 * (T / 64)];
-  const int t = threadIdx.x;
+  __shared__ float lds[2][3][16];
+  const int T = blockDim.x, t = threadIdx.x, waves = T / 64, wave = t >> 6;
+  constexpr bool HOLD = V == 1, HOLDW = V == 1 && !WF;
   const float inv_h = 1.0f / (float)a.H;
+  struct Row {
+    Raw8<BF> b[V];
+    Raw8<XF> x[V], e[V];
+    Raw8<0> dy[V];
+    float rb, rx, g;
+  };
+  auto load_part = [&](Row& r, int m, int i) {
+    const int64_t at = (int64_t)m * a.H + (i * T + t) * 8;
+    r.b[i] = load_raw<BF>(a.blocks[0], at);
+    r.x[i] = load_raw<XF>(a.x, at);
+    r.dy[i] = load_raw<0>(a.dy, at);
+    if (a.dx_out) r.e[i] = load_raw<XF>(a.dx_out, at);
+  };
+  auto load_row = [&](Row& r, int m) {
+    if constexpr (HOLD) {
+      if (t * 8 < a.H) load_part(r, m, 0);
+    }
+    r.rb = a.stats[m];
+    r.rx = a.stats[a.M + m];
+    r.g = a.gate_kind == GATE_TOKEN ? load1_any(a.gate, m, a.w_f32) : 1.0f;
+  };
+  const bool channel = a.gate_kind == GATE_CHANNEL;
   F8 sp[V], sq[V];
+  Raw8<WF> hq, hp, hg;
+  if constexpr (HOLDW) {
+    if (t * 8 < a.H) {
+      hq = load_raw<WF>(a.w_pre, t * 8);
+      hp = load_raw<WF>(a.w_post, t * 8);
+      if (channel) hg = load_raw<WF>(a.gate, t * 8);
+    }
+  }
+  auto w_pre = [&](int h) { return widen<WF>(HOLDW ? hq : load_raw<WF>(a.w_pre, h)); };
+  auto w_post = [&](int h) { return widen<WF>(HOLDW ? hp : load_raw<WF>(a.w_post, h)); };
+  auto gate = [&](int h) { return widen<WF>(HOLDW ? hg : load_raw<WF>(a.gate, h)); };
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sp[i].v[j] = sq[i].v[j] = 0.0f;
+  // bh, xh and e = dx_out + r_x u of one part of the row.
+  auto terms = [&](const Row& r, int64_t at, int h, int i, F8& bh, F8& xh, F8& e, F8& u) {
+    bh = widen<BF>(r.b[i]);
+    add_shards<BF>(bh, a, at);
+    xh = widen<XF>(r.x[i]);
+    u = widen<0>(r.dy[i]);
+    const F8 q = w_pre(h);
+    if (a.dx_out) e = widen<XF>(r.e[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      bh.v[j] *= r.rb;
+      xh.v[j] *= r.rx;
+      u.v[j] *= q.v[j] + a.offset;
+      e.v[j] = (a.dx_out ? e.v[j] : 0.0f) + r.rx * u.v[j];
+    }
+  };
   int par = 0;
+  Row next;
+  load_row(next, blockIdx.x);
   for (int m = blockIdx.x; m < a.M; m += a.groups, par ^= 1) {
     const int64_t row = (int64_t)m * a.H;
-    const float rb = a.stats[m], rx = a.stats[a.M + m];
-    const float g_row = a.gate_kind == GATE_TOKEN ? (a.w_f32 ? reinterpret_cast<const float*>(a.gate)[m]
-                                                             : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.gate)[m] << 16))
-                                                  : 1.0f;
-    F8 bh[V], xh[V], e[V], dy[V];   // e = dx_out + r_x u
+    Row r = next;
+    if (m + a.groups < a.M) load_row(next, m + a.groups);
+    F8 bh, xh, e;
     float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int h = (i * T + t) * 8;
       if (h < a.H) {
-        bh[i] = load_sum8<BF>(a, row + h);
-        xh[i] = load8<XF>(a.x, row + h);
-        dy[i] = load8<0>(a.dy, row + h);
-        if (a.dx_out) {
-          e[i] = load8<XF>(a.dx_out, row + h);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) e[i].v[j] = 0.0f;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int h = (i * T + t) * 8;
-      if (h < a.H) {
-        const F8 wq = load8_any(a.w_pre, h, a.w_f32), wp = load8_any(a.w_post, h, a.w_f32);
+        if constexpr (!HOLD) load_part(r, m, i);
+        F8 u;
+        terms(r, row + h, h, i, bh, xh, e, u);
+        if constexpr (!HOLDW) asm volatile("" ::: "memory");   // the next weights after these are used
+        const F8 w = w_post(h), dy = widen<0>(r.dy[i]);
         F8 g;
-        if (a.gate_kind == GATE_CHANNEL) g = load8_any(a.gate, h, a.w_f32);
+        if (channel) g = gate(h);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          bh[i].v[j] *= rb;
-          xh[i].v[j] *= rx;
-          const float u = dy[i].v[j] * (wq.v[j] + a.offset);
-          e[i].v[j] += rx * u;
-          float k = (wp.v[j] + a.offset) * bh[i].v[j];
-          if (a.gate_kind == GATE_CHANNEL) k *= g.v[j];
-          s[0] += u * xh[i].v[j];
-          s[1] += e[i].v[j] * k;
-          s[2] += rx * xh[i].v[j] * k;
+          float k = (w.v[j] + a.offset) * bh.v[j];
+          if (channel) k *= g.v[j];
+          s[0] += u.v[j] * xh.v[j];
+          s[1] += e.v[j] * k;
+          s[2] += r.rx * xh.v[j] * k;
+          sp[i].v[j] += dy.v[j] * xh.v[j];
         }
+        if constexpr (!HOLD) asm volatile("" ::: "memory");    // one part's loads at a time
       }
     }
-    row_sums<T, 3>(s, lds[par]);   // the other half is still read by slower waves
+    row_sums<3>(s, lds[par], waves, wave);   // the other half is still read by slower waves
     const float c1 = s[0] * inv_h;
     const float vk = a.beta * (s[1] - c1 * s[2]);     // sum(v gate_h w bh), before the token's gate
-    const float c2 = vk * g_row * inv_h;
-    const float bg = a.beta * g_row;
+    const float c2 = vk * r.g * inv_h;
+    const float bg = a.beta * r.g;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int h = (i * T + t) * 8;
       if (h < a.H) {
-        const F8 wp = load8_any(a.w_post, h, a.w_f32);
-        F8 g;
-        if (a.gate_kind == GATE_CHANNEL) g = load8_any(a.gate, h, a.w_f32);
-        F8 dx, db;
+        if constexpr (!HOLD) {
+          F8 u;
+          load_part(r, m, i);
+          terms(r, row + h, h, i, bh, xh, e, u);
+        }
+        const F8 w = w_post(h);
+        F8 g, dx, db;
+        if (channel) g = gate(h);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float dt = e[i].v[j] - rx * c1 * xh[i].v[j];
+          const float dt = e.v[j] - r.rx * c1 * xh.v[j];
           const float v = bg * dt;
-          float z = v * (wp.v[j] + a.offset);
-          if (a.gate_kind == GATE_CHANNEL) z *= g.v[j];
+          float z = v * (w.v[j] + a.offset);
+          if (channel) z *= g.v[j];
           dx.v[j] = a.alpha * dt;
-          db.v[j] = rb * (z - bh[i].v[j] * c2);
-          sp[i].v[j] += dy[i].v[j] * xh[i].v[j];
-          sq[i].v[j] += v * bh[i].v[j];
+          db.v[j] = r.rb * (z - bh.v[j] * c2);
+          sq[i].v[j] += v * bh.v[j];
         }
         store8<XF>(a.x_out, row + h, dx);
         store8<0>(a.y, row + h, db);
+        if constexpr (!HOLD) asm volatile("" ::: "memory");
       }
     }
     if (a.gate_kind == GATE_TOKEN && t == 0) a.dgate[m] = vk;
@@ -304,55 +364,57 @@ __global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs args) {
 }
 
 // Columns 4 c .. 4 c + 3 of both sums over the workgroups of the row pass: 16
-// threads along the columns, 16 strips of workgroups, joined through LDS.
-__global__ __launch_bounds__(256) void norm_columns_kernel(NormArgs args) {
+// threads along the columns, 64 strips of workgroups, joined through LDS.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(NormArgs args) {
   (void)args;
   const NormArgs& a = norm_kernarg<NormArgs>();
-  __shared__ f32x4_t lds[16][17];
+  __shared__ f32x4_t lds[64][17];
   const int c = threadIdx.x & 15, strip = threadIdx.x >> 4;
   const int h = (blockIdx.x * 16 + c) * 4;
   const int which = blockIdx.y;
   f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (h < a.H)
-    for (int g = strip; g < a.groups; g += 16)
-      s += *reinterpret_cast<const f32x4_t*>(a.partial + ((int64_t)g * 2 + which) * a.H + h);
+  if (h < a.H) {
+    const float* base = a.partial + (int64_t)which * a.H + h;
+    const int64_t stride = (int64_t)2 * a.H;
+#pragma unroll 4
+    for (int g = strip; g < a.groups; g += 64) s += *reinterpret_cast<const f32x4_t*>(base + g * stride);
+  }
   lds[strip][c] = s;
+  __syncthreads();
+  if (strip < 8) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += lds[strip + 8 * k][c];
+    lds[strip][c] = s;
+  }
   __syncthreads();
   if (strip != 0 || h >= a.H) return;
 #pragma unroll
-  for (int k = 1; k < 16; ++k) s += lds[k][c];
+  for (int k = 1; k < 8; ++k) s += lds[k][c];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int i = h + j;
     if (which == 0) {
       a.dw_pre[i] = s[j];
     } else if (a.gate_kind == GATE_CHANNEL) {
-      const float w = (a.w_f32 ? reinterpret_cast<const float*>(a.w_post)[i]
-                               : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.w_post)[i] << 16)) +
-                      a.offset;
-      const float g = a.w_f32 ? reinterpret_cast<const float*>(a.gate)[i]
-                              : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(a.gate)[i] << 16);
-      a.dw_post[i] = g * s[j];
-      a.dgate[i] = w * s[j];
+      a.dw_post[i] = load1_any(a.gate, i, a.w_f32) * s[j];
+      a.dgate[i] = (load1_any(a.w_post, i, a.w_f32) + a.offset) * s[j];
     } else {
       a.dw_post[i] = s[j];
     }
   }
 }
 
+template <int XF, int BF, int V>
+static void launch_norm_v(const NormArgs& a, hipStream_t s) {
+  const int T = norm_threads<V>(a.H), rows = T == 64 ? kNormRows : 1;
+  hipLaunchKernelGGL((block_norm_kernel<XF, BF, V>), dim3((a.M + rows - 1) / rows), dim3(T, rows), 0, s, a);
+}
+
 template <int XF, int BF>
 static void launch_norm_t(const NormArgs& a, hipStream_t s) {
-#define TPF_NORM(T, V)                                                                                          \
-  hipLaunchKernelGGL((block_norm_kernel<XF, BF, T, V>), dim3((a.M + norm_rows<T>() - 1) / norm_rows<T>()),     \
-                     dim3(T * norm_rows<T>()), 0, s, a)
-  if (a.H <= 512) TPF_NORM(64, 1);
-  else if (a.H <= 1024) TPF_NORM(64, 2);
-  else if (a.H <= 2048) TPF_NORM(256, 1);
-  else if (a.H <= 4096) TPF_NORM(256, 2);
-  else if (a.H <= 8192) TPF_NORM(512, 2);
-  else if (a.H <= 16384) TPF_NORM(1024, 2);
-  else TPF_NORM(1024, 4);
-#undef TPF_NORM
+  if (a.H <= 8192) launch_norm_v<XF, BF, 1>(a, s);
+  else if (a.H <= 16384) launch_norm_v<XF, BF, 2>(a, s);
+  else launch_norm_v<XF, BF, 4>(a, s);
 }
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
@@ -366,22 +428,29 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// As many workgroups as the GPU's 256 compute units hold at 16 waves each,
+// but at least eight rows a workgroup once every unit has one: each workgroup
+// leaves 8 H bytes of column sums.
 int norm_backward_groups(int64_t M, int64_t H) {
-  (void)H;
-  return (int)std::min<int64_t>(M, 512);
+  const int waves = std::min<int>(16, norm_threads<1>((int)H) / 64);
+  const int64_t cap = 256 * (16 / waves);
+  return (int)std::max(std::min<int64_t>(M, 256), std::min(cap, M / 8));
+}
+
+template <int XF, int BF, int WF>
+static void launch_norm_bwd_w(const NormArgs& a, hipStream_t s) {
+#define TPF_NORM(V) \
+  hipLaunchKernelGGL((block_norm_backward_kernel<XF, BF, WF, V>), dim3(a.groups), dim3(norm_threads<V>(a.H)), 0, s, a)
+  if (a.H <= 8192) TPF_NORM(1);
+  else if (a.H <= 16384) TPF_NORM(2);
+  else TPF_NORM(4);
+#undef TPF_NORM
 }
 
 template <int XF, int BF>
 static void launch_norm_bwd_t(const NormArgs& a, hipStream_t s) {
-#define TPF_NORM(T, V) \
-  hipLaunchKernelGGL((block_norm_backward_kernel<XF, BF, T, V>), dim3(a.groups), dim3(T), 0, s, a)
-  if (a.H <= 512) TPF_NORM(64, 1);
-  else if (a.H <= 2048) TPF_NORM(256, 1);
-  else if (a.H <= 4096) TPF_NORM(512, 1);
-  else if (a.H <= 8192) TPF_NORM(1024, 1);
-  else if (a.H <= 16384) TPF_NORM(1024, 2);
-  else TPF_NORM(1024, 4);
-#undef TPF_NORM
+  if (a.w_f32) launch_norm_bwd_w<XF, BF, 1>(a, s);
+  else launch_norm_bwd_w<XF, BF, 0>(a, s);
 }
 
 hipError_t launch_block_norm_backward(const NormArgs& a, hipStream_t s) {
@@ -396,7 +465,7 @@ hipError_t launch_block_norm_backward(const NormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_norm_columns(const NormArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(norm_columns_kernel, dim3((a.H + 63) / 64, 2), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(norm_columns_kernel, dim3((a.H + 63) / 64, 2), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 

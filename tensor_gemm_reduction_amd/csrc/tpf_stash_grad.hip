@@ -204,16 +204,17 @@ __global__ __launch_bounds__(Cfg::THREADS) void stash_grad_kernel(StashGradArgs 
   // The scales of up to kSgSteps steps at a time; almost every call has one round.
   for (int b0 = s0; b0 < s1; b0 += kSgSteps) {
     const int b1 = min(b0 + kSgSteps, s1);
-    const int words = (b1 - b0 + 1) * 2 * S::RB;     // a step more: its words are fetched, not used
-    for (int i = threadIdx.x; i < words; i += Cfg::THREADS) {
-      const int band = b0 * 2 + i / S::RB, col = (r0 >> 5) + i % S::RB;
-      scale_slot<Cfg>()[i] = band < bands && col < nsc ? a.scales[k][(int64_t)band * nsc + col] : 0;
-    }
     ld.last = b1 - 1;
 #pragma unroll
     for (int q = 0; q < S::LOADS; ++q) ld.load(q_slot<Cfg, 0>(), b_slot<Cfg, 0>(), b0, q);
 #pragma unroll
     for (int q = 0; q < S::LOADS; ++q) ld.load(q_slot<Cfg, 1>(), b_slot<Cfg, 1>(), b0 + 1, q);
+    // Behind the first tiles' loads, so that one latency covers both.
+    const int words = (b1 - b0 + 1) * 2 * S::RB;     // a step more: its words are fetched, not used
+    for (int i = threadIdx.x; i < words; i += Cfg::THREADS) {
+      const int band = b0 * 2 + i / S::RB, col = (r0 >> 5) + i % S::RB;
+      scale_slot<Cfg>()[i] = band < bands && col < nsc ? a.scales[k][(int64_t)band * nsc + col] : 0;
+    }
     wait_vmcnt(S::LOADS);
     lds_barrier();
     SgSlice<Cfg> d[2];
