@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import time
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +16,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libtpfuse.so")
+ARGS = os.path.join(LIBDIR, "_args.so")      # the Python binding's native argument checks
 
 SOURCES = ["tpf_kernels.hip", "tpf_api.cpp", "tpf_block_api.cpp", "tpf_norm.hip", "tpf_stash.hip",
            "tpf_stash_grad.hip", "tpf_qweight.hip"]
@@ -58,14 +60,26 @@ def _compile_jobs(cc: str):
     return jobs
 
 
+def _args_command(out: str):
+    """Compile command of the argument checks: host code against torch's headers."""
+    import torch
+    from torch.utils import cpp_extension
+    include = cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]
+    return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             os.path.join(CSRC, "tpf_args.cpp"), "-o", out] + [f"-I{i}" for i in include]
+            + ["-L" + cpp_extension.TORCH_LIB_PATH, "-ltorch_python", "-ltorch_cpu", "-lc10"])
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source for gfx950 and link libtpfuse.so; returns its path."""
+    """Compile every source for gfx950, link libtpfuse.so and the binding's
+    argument checks; returns the library's path."""
     os.makedirs(LIBDIR, exist_ok=True)
     cc = hipcc()
     t0 = time.time()
     jobs = _compile_jobs(cc)
     procs = []
-    for name, obj, cmd in jobs:
+    for name, obj, cmd in jobs + [("tpf_args.cpp", ARGS, _args_command(ARGS + ".tmp"))]:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
@@ -73,7 +87,7 @@ def build(verbose: bool = False) -> str:
     for name, pr in procs:
         out, err = pr.communicate()
         if pr.returncode != 0:
-            failed.append(f"hipcc failed on {name}:\n{out}\n{err}")
+            failed.append(f"compiling {name} failed:\n{out}\n{err}")
         elif verbose and err.strip():
             print(err, file=sys.stderr)
     if failed:
@@ -85,6 +99,7 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(ARGS + ".tmp", ARGS)
     for o in objs:
         os.remove(o)
     if verbose:

@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import List, Optional, Sequence
 
@@ -16,6 +18,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libtpfuse.so")
+ARGS_PATH = os.path.join(_HERE, "lib", "_args.so")
 
 # Status codes, dtypes, schedulers, semantics and op ids (include/tpfuse.h).
 OK = 0
@@ -36,7 +39,7 @@ SCHEDS = {"auto": SCHED_AUTO, "persistent": SCHED_PERSISTENT, "two_stream": SCHE
           "tile": SCHED_TILE, "fold": SCHED_FOLD, "stationary": SCHED_STATIONARY}
 
 _VP = ctypes.c_void_p
-_PP = ctypes.POINTER(ctypes.c_void_p)
+_PP = ctypes.c_void_p      # an array of addresses: a ctypes array, or bytes from `_operands`
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
@@ -79,6 +82,7 @@ SIGNATURES = {
 }
 
 _lib: Optional[ctypes.CDLL] = None
+_args = None                # the native argument checks (csrc/tpf_args.cpp)
 
 
 class TpfError(RuntimeError):
@@ -89,17 +93,22 @@ class TpfError(RuntimeError):
 
 def load() -> ctypes.CDLL:
     """Load the in-tree libtpfuse.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _args
     if _lib is not None:
         return _lib
-    if not os.path.exists(LIB_PATH):
-        raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m tensor_gemm_reduction_amd.build`")
+    for path in (LIB_PATH, ARGS_PATH):
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m tensor_gemm_reduction_amd.build`")
+    spec = importlib.util.spec_from_file_location(
+        "_args", ARGS_PATH, loader=importlib.machinery.ExtensionFileLoader("_args", ARGS_PATH))
+    native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(native)
     lib = ctypes.CDLL(LIB_PATH, mode=ctypes.RTLD_GLOBAL)
     for name, (res, args) in SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    _lib = lib
+    _args, _lib = native, lib
     return lib
 
 
@@ -550,15 +559,15 @@ def _ptrs(ts):
     return (_VP * len(ts))(*[t.data_ptr() for t in ts])
 
 
-def _all_ok(ts, idx: int, dtype, shape) -> bool:
-    """Whether every tensor is on GPU `idx`, contiguous, of one dtype and shape.
+def _operands(idx: int, *groups):
+    """Addresses of each group's tensors (tensors, dtype, shape, ...), or None
+    where one is not a contiguous tensor on GPU `idx` of that dtype and shape.
 
     Decode-sized calls run for a few microseconds on the GPU, so the checks of
-    good arguments are this one pass; `_check` names what is wrong."""
-    for t in ts:
-        if t.get_device() != idx or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-            return False
-    return True
+    good arguments are this one native pass; `_check` names what is wrong."""
+    if _args is None:
+        load()
+    return _args.operands(idx, *groups)
 
 
 def _ctx(handle: Optional[Handle], dev, stream):
@@ -570,30 +579,29 @@ def _ctx(handle: Optional[Handle], dev, stream):
     return h._h, sp
 
 
-def _shards(p: int, shape, dtype, dev):
-    """p new tensors of one shape, from one allocation while that keeps them aligned."""
-    size = dtype.itemsize
-    for n in shape:
-        size *= n
-    if size % 16 == 0 or dtype is torch.uint8:
-        return torch.empty((p, *shape), dtype=dtype, device=dev).unbind(0)
-    return [torch.empty(shape, dtype=dtype, device=dev) for _ in range(p)]
+def _empty(dev, *groups):
+    """New tensors (dtype, shape, ...) on GPU `dev`; None for a shape of None."""
+    if _args is None:
+        load()
+    return _args.empty(dev.index, *groups)
 
 
 def _norm_operands(x, blocks, w_pre, w_post, gate):
-    """Checks shared by the norm's two directions; returns (device, M, H, gate kind)."""
+    """Checks shared by the norm's two directions; returns (device, M, H, gate kind, the
+    blocks' addresses)."""
     p = len(blocks)
     _need(p >= 1, "blocks: no tensors given")
     _need(x.dim() == 2, f"x has {x.dim()} dimensions, expected [M, H]")
     M, H = x.shape
     dev, idx = x.device, x.get_device()
     kind = GATE_NONE if gate is None else GATE_TOKEN if gate.dim() == 2 else GATE_CHANNEL
-    vec = (H,)
-    if (idx >= 0 and x.dtype in OUT_DTYPES and x.is_contiguous() and blocks[0].dtype in OUT_DTYPES
-            and _all_ok(blocks, idx, blocks[0].dtype, x.shape) and w_pre.dtype in OUT_DTYPES
-            and _all_ok((w_pre, w_post), idx, w_pre.dtype, vec)
-            and (gate is None or _all_ok((gate,), idx, w_pre.dtype, (M, 1) if kind == GATE_TOKEN else vec))):
-        return dev, M, H, kind
+    vec, rows = (H,), (M, H)
+    b, w = blocks[0].dtype, w_pre.dtype
+    if x.dtype in OUT_DTYPES and b in OUT_DTYPES and w in OUT_DTYPES:
+        got = _operands(idx, blocks, b, rows, (x,), x.dtype, rows, (w_pre, w_post), w, vec,
+                        () if gate is None else (gate,), w, (M, 1) if kind == GATE_TOKEN else vec)
+        if got is not None:
+            return dev, M, H, kind, got[0]
     _check("x", [x], (M, H), OUT_DTYPES)
     _check("blocks", blocks, (M, H), OUT_DTYPES, dev)
     _need(all(b.dtype == blocks[0].dtype for b in blocks), "blocks: the tensors differ in dtype")
@@ -601,7 +609,7 @@ def _norm_operands(x, blocks, w_pre, w_post, gate):
     _check("w_post", [w_post], (H,), (w_pre.dtype,), dev)
     if gate is not None:
         _check("gate", [gate], (M, 1) if kind == GATE_TOKEN else (H,), (w_pre.dtype,), dev)
-    return dev, M, H, kind
+    return dev, M, H, kind, _ptrs(blocks)
 
 
 def block_norm(x: torch.Tensor, blocks: Sequence[torch.Tensor], w_pre: torch.Tensor, w_post: torch.Tensor,
@@ -618,19 +626,17 @@ def block_norm(x: torch.Tensor, blocks: Sequence[torch.Tensor], w_pre: torch.Ten
     `gate` is None, [H] (one factor a channel) or [M, 1] (one a token); weights
     are stored as offsets from 1 with `unit_offset`.  `stats` ([2, M] fp32, for
     `block_norm_backward`) is None unless `want_stats`."""
-    dev, M, H, kind = _norm_operands(x, blocks, w_pre, w_post, gate)
+    dev, M, H, kind, at = _norm_operands(x, blocks, w_pre, w_post, gate)
     if x_out is not None:
         _check("x_out", [x_out], (M, H), (x.dtype,), dev)
     if y is not None:
         _check("y", [y], (M, H), (torch.bfloat16,), dev)
     with _on(stream):
-        if x_out is None:
-            x_out = torch.empty_like(x)
-        if y is None:
-            y = torch.empty_like(x, dtype=torch.bfloat16)
-        stats = torch.empty((2, M), dtype=torch.float32, device=dev) if want_stats else None
+        new_x, new_y, stats = _empty(dev, x.dtype, (M, H) if x_out is None else None, torch.bfloat16,
+                                     (M, H) if y is None else None, torch.float32, (2, M) if want_stats else None)
+        x_out, y = new_x if x_out is None else x_out, new_y if y is None else y
     h, sp = _ctx(handle, dev, stream)
-    check(load().tpf_block_norm(h, len(blocks), M, H, x.data_ptr(), _dtype_code(x.dtype), _ptrs(blocks),
+    check(load().tpf_block_norm(h, len(blocks), M, H, x.data_ptr(), _dtype_code(x.dtype), at,
                                 _dtype_code(blocks[0].dtype), w_pre.data_ptr(), w_post.data_ptr(),
                                 gate.data_ptr() if gate is not None else None, kind, _dtype_code(w_pre.dtype), alpha,
                                 beta, eps, 1 if unit_offset else 0, x_out.data_ptr(), y.data_ptr(),
@@ -648,25 +654,24 @@ def block_norm_backward(dy: torch.Tensor, dx_out: Optional[torch.Tensor], x: tor
     `dy` is the gradient of y, `dx_out` that of x_out from what else reads it
     (None: nothing), `x` the forward's x_out, `stats` its statistics.  `db` is
     the gradient of every tensor of `blocks`; `dgate` has the gate's shape."""
-    dev, M, H, kind = _norm_operands(x, blocks, w_pre, w_post, gate)
-    _check("dy", [dy], (M, H), (torch.bfloat16,), dev)
-    if dx_out is not None:
-        _check("dx_out", [dx_out], (M, H), (x.dtype,), dev)
-    _check("stats", [stats], (2, M), (torch.float32,), dev)
+    dev, M, H, kind, at = _norm_operands(x, blocks, w_pre, w_post, gate)
+    if _operands(dev.index, (dy,), torch.bfloat16, (M, H), () if dx_out is None else (dx_out,), x.dtype, (M, H),
+                 (stats,), torch.float32, (2, M)) is None:
+        _check("dy", [dy], (M, H), (torch.bfloat16,), dev)
+        if dx_out is not None:
+            _check("dx_out", [dx_out], (M, H), (x.dtype,), dev)
+        _check("stats", [stats], (2, M), (torch.float32,), dev)
     _check_ws(ws, dev)
     need = load().tpf_block_norm_backward_ws(M, H)
     with _on(stream):
-        dx = torch.empty_like(x)
-        db = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
-        dw_pre = torch.empty(H, dtype=torch.float32, device=dev)
-        dw_post = torch.empty(H, dtype=torch.float32, device=dev)
-        dgate = torch.empty(gate.shape, dtype=torch.float32, device=dev) if gate is not None else None
-        if ws is None:
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        dx, db, dw_pre, dw_post, dgate, new_ws = _empty(
+            dev, x.dtype, (M, H), torch.bfloat16, (M, H), torch.float32, (H,), torch.float32, (H,), torch.float32,
+            None if gate is None else tuple(gate.shape), torch.uint8, (max(need, 16),) if ws is None else None)
+        ws = new_ws if ws is None else ws
     h, sp = _ctx(handle, dev, stream)
     check(load().tpf_block_norm_backward(
         h, len(blocks), M, H, dy.data_ptr(), dx_out.data_ptr() if dx_out is not None else None, x.data_ptr(),
-        _dtype_code(x.dtype), _ptrs(blocks), _dtype_code(blocks[0].dtype), stats.data_ptr(), w_pre.data_ptr(),
+        _dtype_code(x.dtype), at, _dtype_code(blocks[0].dtype), stats.data_ptr(), w_pre.data_ptr(),
         w_post.data_ptr(), gate.data_ptr() if gate is not None else None, kind, _dtype_code(w_pre.dtype), alpha, beta,
         1 if unit_offset else 0, dx.data_ptr(), db.data_ptr(), dw_pre.data_ptr(), dw_post.data_ptr(),
         dgate.data_ptr() if dgate is not None else None, ws.data_ptr(), ws.numel() * ws.element_size(),
@@ -689,14 +694,16 @@ def stash_pack(u: Sequence[torch.Tensor], gelu: bool = True, handle: Optional[Ha
     _need(u[0].dim() == 2, f"u[0] has {u[0].dim()} dimensions, expected [M, F]")
     M, F = u[0].shape
     dev = u[0].device
-    if not (u[0].is_cuda and _all_ok(u, u[0].get_device(), torch.bfloat16, (M, F))):
+    at = _operands(u[0].get_device(), u, torch.bfloat16, (M, F))
+    if at is None:
         _check("u", u, (M, F))
+        at = (_ptrs(u),)
     with _on(stream):
-        codes = _shards(p, (M, F), torch.float8_e4m3fn, dev)
-        scales = _shards(p, _stash_shape(M, F), torch.uint8, dev)
-        h = _shards(p, (M, F), torch.bfloat16, dev) if gelu else None
+        new = _empty(dev, *((torch.float8_e4m3fn, (M, F)) * p + (torch.uint8, _stash_shape(M, F)) * p
+                            + (torch.bfloat16, (M, F)) * (p if gelu else 0)))
+    codes, scales, h = new[:p], new[p:2 * p], new[2 * p:] if gelu else None
     hd, sp = _ctx(handle, dev, stream)
-    check(load().tpf_stash_pack(hd, p, M, F, _ptrs(u), 1 if gelu else 0, _ptrs(h) if gelu else None,
+    check(load().tpf_stash_pack(hd, p, M, F, at[0], 1 if gelu else 0, _ptrs(h) if gelu else None,
                                 _ptrs(codes), _ptrs(scales), sp))
     return h, codes, scales
 
@@ -707,26 +714,32 @@ def _check_stash(codes, scales):
     _need(codes[0].dim() == 2, f"codes[0] has {codes[0].dim()} dimensions, expected [M, F]")
     M, F = codes[0].shape
     _check_shards("scales", scales, p)
-    dev, idx = codes[0].device, codes[0].get_device()
-    if not (idx >= 0 and codes[0].dtype in CODE_DTYPES and _all_ok(codes, idx, codes[0].dtype, (M, F))
-            and _all_ok(scales, idx, torch.uint8, _stash_shape(M, F))):
+    dev = codes[0].device
+    at = None
+    if codes[0].dtype in CODE_DTYPES:
+        at = _operands(codes[0].get_device(), codes, codes[0].dtype, (M, F), scales, torch.uint8, _stash_shape(M, F))
+    if at is None:
         _check("codes", codes, (M, F), CODE_DTYPES)
         _check("scales", scales, _stash_shape(M, F), (torch.uint8,), dev)
-    return dev, p, M, F
+        at = _ptrs(codes), _ptrs(scales)
+    return dev, p, M, F, at
 
 
 def stash_backward(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tensor], dh: Sequence[torch.Tensor],
                    handle: Optional[Handle] = None, stream=None):
     """(du, h): GeLU's gradient du[k] = dh[k] GeLU'(u) and its value h[k] =
     GeLU(u), u the 8-bit activations of `stash_pack`."""
-    dev, p, M, F = _check_stash(codes, scales)
+    dev, p, M, F, at = _check_stash(codes, scales)
     _check_shards("dh", dh, p)
-    if not _all_ok(dh, dev.index, torch.bfloat16, (M, F)):
+    dat = _operands(dev.index, dh, torch.bfloat16, (M, F))
+    if dat is None:
         _check("dh", dh, (M, F), device=dev)
+        dat = (_ptrs(dh),)
     with _on(stream):
-        du, h = _shards(p, (M, F), torch.bfloat16, dev), _shards(p, (M, F), torch.bfloat16, dev)
+        new = _empty(dev, *((torch.bfloat16, (M, F)) * (2 * p)))
+    du, h = new[:p], new[p:]
     hd, sp = _ctx(handle, dev, stream)
-    check(load().tpf_stash_backward(hd, p, M, F, _ptrs(codes), _ptrs(scales), _ptrs(dh), _ptrs(du), _ptrs(h),
+    check(load().tpf_stash_backward(hd, p, M, F, *at, dat[0], _ptrs(du), _ptrs(h),
                                     sp))
     return du, h
 
@@ -736,23 +749,28 @@ def stash_weight_grad(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tens
                       handle: Optional[Handle] = None, stream=None) -> List[torch.Tensor]:
     """dW[k] = U_k^T dY[k], U_k [M, R] the 8-bit activations of `stash_pack`:
     `weight_grad` of an input kept in 8 bits."""
-    dev, p, M, R = _check_stash(codes, scales)
+    dev, p, M, R, at = _check_stash(codes, scales)
     _check_shards("dY", dY, p)
     C = dY[0].shape[1]
-    _check("dY", dY, (M, C), device=dev)
+    yat = _operands(dev.index, dY, torch.bfloat16, (M, C))
+    if yat is None:
+        _check("dY", dY, (M, C), device=dev)
+        yat = (_ptrs(dY),)
     if dW is None:
+        _need(out_dtype in OUT_DTYPES, f"output dtype must be bfloat16 or float32, got {out_dtype}")
         with _on(stream):
-            dW = [torch.empty((R, C), dtype=out_dtype, device=dev) for _ in range(p)]
-    _check_shards("dW", dW, p)
-    _check("dW", dW, (R, C), OUT_DTYPES, dev)
-    _need(all(d.dtype == dW[0].dtype for d in dW), "dW: the shards differ in dtype")
+            dW = list(_empty(dev, *((out_dtype, (R, C)) * p)))
+    else:
+        _check_shards("dW", dW, p)
+        _check("dW", dW, (R, C), OUT_DTYPES, dev)
+        _need(all(d.dtype == dW[0].dtype for d in dW), "dW: the shards differ in dtype")
     _check_ws(ws, dev)
     need = load().tpf_stash_weight_grad_ws(p, M, R, C)
     if ws is None and need:
         with _on(stream):
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws, = _empty(dev, torch.uint8, (need,))
     hd, sp = _ctx(handle, dev, stream)
-    check(load().tpf_stash_weight_grad(hd, p, M, R, C, _ptrs(codes), _ptrs(scales), _ptrs(dY), _ptrs(dW),
+    check(load().tpf_stash_weight_grad(hd, p, M, R, C, *at, yat[0], _ptrs(dW),
                                        _dtype_code(dW[0].dtype), ws.data_ptr() if ws is not None else None,
                                        ws.numel() * ws.element_size() if ws is not None else 0, sp))
     return dW
@@ -779,29 +797,30 @@ def qweight_matmul(X: Sequence[torch.Tensor], codes: Sequence[torch.Tensor], sca
     if zeros is not None:
         _check_shards("zeros", zeros, p)
     N, per_group = codes[0].shape[0], (codes[0].shape[0], K // group)
-    dev, idx = X[0].device, X[0].get_device()
-    if not (idx >= 0 and _all_ok(X, idx, torch.bfloat16, (M, K)) and _all_ok(codes, idx, torch.uint8, (N, K // 2))
-            and _all_ok(scales, idx, torch.bfloat16, per_group)
-            and (zeros is None or _all_ok(zeros, idx, torch.uint8, per_group))):
+    dev = X[0].device
+    at = _operands(X[0].get_device(), X, torch.bfloat16, (M, K), codes, torch.uint8, (N, K // 2), scales, torch.bfloat16,
+                   per_group, () if zeros is None else zeros, torch.uint8, per_group)
+    if at is None:
         _check("X", X, (M, K))
         _check("codes", codes, (N, K // 2), (torch.uint8,), dev)
         _check("scales", scales, per_group, (torch.bfloat16,), dev)
         if zeros is not None:
             _check("zeros", zeros, per_group, (torch.uint8,), dev)
+        at = _ptrs(X), _ptrs(codes), _ptrs(scales), None if zeros is None else _ptrs(zeros)
     if Y is None:
         _need(out_dtype in OUT_DTYPES, f"output dtype must be bfloat16 or float32, got {out_dtype}")
         with _on(stream):
-            Y = torch.empty((M, N), dtype=out_dtype, device=dev)
+            Y, = _empty(dev, out_dtype, (M, N))
     else:
         _check("Y", [Y], (M, N), OUT_DTYPES, dev)
     _check_ws(ws, dev)
     need = load().tpf_qweight_matmul_ws(p, M, K, N, group)
     if ws is None and need:
         with _on(stream):
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws, = _empty(dev, torch.uint8, (need,))
     hd, sp = _ctx(handle, dev, stream)
-    check(load().tpf_qweight_matmul(hd, p, M, K, N, group, _ptrs(X), _ptrs(codes), _ptrs(scales),
-                                    _ptrs(zeros) if zeros is not None else None, 1 if gelu else 0, Y.data_ptr(),
+    check(load().tpf_qweight_matmul(hd, p, M, K, N, group, at[0], at[1], at[2],
+                                    None if zeros is None else at[3], 1 if gelu else 0, Y.data_ptr(),
                                     _dtype_code(Y.dtype), ws.data_ptr() if ws is not None else None,
                                     ws.numel() * ws.element_size() if ws is not None else 0, sp))
     return Y
