@@ -15,7 +15,15 @@ enum GateKind : int { GATE_NONE = 0, GATE_CHANNEL = 1, GATE_TOKEN = 2 };
 
 constexpr int kNormMaxH = 32768;     // a row is held in one workgroup's registers
 constexpr int kStashBlock = 32;      // 8-bit activations: one scale per 32 x 32 values
-constexpr int kQwMaxRows = 64;       // rows of X one workgroup of the 4-bit product holds
+
+// Outputs of this many bytes and more, the memory-side cache's size, are stored
+// past the caches: no reader finds them there, and on their way through they
+// cost lines still to be read (norm backward of 8192 x 8192 160 -> 155 us, GeLU
+// backward of 8 x 2048 x 6144 128 -> 122).  Smaller ones stay for the kernel that
+// reads them next: past the caches a norm of 4096 x 4096 takes 24.5 us by itself
+// instead of 28.1, but norm, matrix product and norm of 2048 x 8192 216 instead of
+// 204 and of 4096 x 8192 270 instead of 259.
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 
 // ---------------------------------------------------------------------------
 // Norms.
@@ -61,7 +69,7 @@ struct StashArgs {
   void* du[kMaxShards];              // backward: [M][F] bf16
   int p, M, F;
 };
-hipError_t launch_stash_pack(const StashArgs& a, int gelu, int num_cus, hipStream_t s);
+hipError_t launch_stash_pack(const StashArgs& a, int gelu, hipStream_t s);
 hipError_t launch_stash_backward(const StashArgs& a, int num_cus, hipStream_t s);
 
 struct StashGradArgs {

@@ -240,7 +240,7 @@ int tpf_stash_pack(tpf_handle h, int p, int64_t M, int64_t F, const void* const*
     a.M = (int)M;
     a.F = (int)F;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    TPF_TIMED(h, s, launch_stash_pack(a, gelu, h->num_cus, s));
+    TPF_TIMED(h, s, launch_stash_pack(a, gelu, s));
     return TPF_OK;
   });
 }

@@ -63,17 +63,23 @@ __device__ __forceinline__ float load1_any(const void* base, int64_t e, int f32)
              : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[e] << 16);
 }
 
-template <int F32>
+template <int STREAM, class V>
+__device__ __forceinline__ void put(V* p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
+template <int F32, int STREAM>
 __device__ __forceinline__ void store8(void* base, int64_t e, const F8& x) {
   if constexpr (F32) {
     f32x4_t* q = reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(base) + e);
-    q[0] = f32x4_t{x.v[0], x.v[1], x.v[2], x.v[3]};
-    q[1] = f32x4_t{x.v[4], x.v[5], x.v[6], x.v[7]};
+    put<STREAM>(q, f32x4_t{x.v[0], x.v[1], x.v[2], x.v[3]});
+    put<STREAM>(q + 1, f32x4_t{x.v[4], x.v[5], x.v[6], x.v[7]});
   } else {
     bf16x8_t h;
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = (__bf16)x.v[i];
-    *reinterpret_cast<bf16x8_t*>(reinterpret_cast<uint16_t*>(base) + e) = h;
+    put<STREAM>(reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(base) + e), __builtin_bit_cast(u32x4_t, h));
   }
 }
 
@@ -132,7 +138,7 @@ static int norm_threads(int H) {
   return (H + 512 * V - 1) / (512 * V) * 64;
 }
 
-template <int XF, int BF, int V>
+template <int XF, int BF, int V, int STREAM>
 __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs args) {
   (void)args;
   const NormArgs& a = norm_kernarg<NormArgs>();
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs args) {
         x[i].v[j] = o;
         s[0] += o * o;
       }
-      store8<XF>(a.x_out, row + h, x[i]);
+      store8<XF, STREAM>(a.x_out, row + h, x[i]);
     }
   }
   row_sums<1>(s, lds[1], waves, wave);
@@ -196,7 +202,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs args) {
       const F8 w = load8_any(a.w_pre, h, a.w_f32);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[i].v[j] = x[i].v[j] * rx * (w.v[j] + a.offset);
-      store8<0>(a.y, row + h, x[i]);
+      store8<0, STREAM>(a.y, row + h, x[i]);
     }
   }
   if (a.stats && t == 0) {
@@ -224,7 +230,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs args) {
 // and keeps its columns' bf16 weights and gate.  16 waves leave 128 registers a
 // thread: longer rows are read again from the cache after the sums instead of
 // being held, and so are fp32 weights.
-template <int XF, int BF, int WF, int V>
+template <int XF, int BF, int WF, int V, int STREAM>
 __global__ __launch_bounds__(1024) void block_norm_backward_kernel(NormArgs args) {
   (void)args;
   const NormArgs& a = norm_kernarg<NormArgs>();
@@ -345,8 +351,8 @@ __global__ __launch_bounds__(1024) void block_norm_backward_kernel(NormArgs args
           db.v[j] = r.rb * (z - bh.v[j] * c2);
           sq[i].v[j] += v * bh.v[j];
         }
-        store8<XF>(a.x_out, row + h, dx);
-        store8<0>(a.y, row + h, db);
+        store8<XF, STREAM>(a.x_out, row + h, dx);
+        store8<0, STREAM>(a.y, row + h, db);
         if constexpr (!HOLD) asm volatile("" ::: "memory");
       }
     }
@@ -357,8 +363,8 @@ __global__ __launch_bounds__(1024) void block_norm_backward_kernel(NormArgs args
   for (int i = 0; i < V; ++i) {
     const int h = (i * T + t) * 8;
     if (h < a.H) {
-      store8<1>(out, h, sp[i]);
-      store8<1>(out + a.H, h, sq[i]);
+      store8<1, 0>(out, h, sp[i]);
+      store8<1, 0>(out + a.H, h, sq[i]);
     }
   }
 }
@@ -404,10 +410,18 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(NormArgs args) {
   }
 }
 
+// Whether both [M][H] outputs are stored past the caches.
+template <int XF>
+static bool norm_streams(const NormArgs& a) {
+  return (int64_t)a.M * a.H * (XF ? 6 : 4) >= kStreamBytes;
+}
+
 template <int XF, int BF, int V>
 static void launch_norm_v(const NormArgs& a, hipStream_t s) {
   const int T = norm_threads<V>(a.H), rows = T == 64 ? kNormRows : 1;
-  hipLaunchKernelGGL((block_norm_kernel<XF, BF, V>), dim3((a.M + rows - 1) / rows), dim3(T, rows), 0, s, a);
+  const dim3 grid((a.M + rows - 1) / rows), block(T, rows);
+  if (norm_streams<XF>(a)) hipLaunchKernelGGL((block_norm_kernel<XF, BF, V, 1>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((block_norm_kernel<XF, BF, V, 0>), grid, block, 0, s, a);
 }
 
 template <int XF, int BF>
@@ -439,11 +453,20 @@ int norm_backward_groups(int64_t M, int64_t H) {
 
 template <int XF, int BF, int WF>
 static void launch_norm_bwd_w(const NormArgs& a, hipStream_t s) {
-#define TPF_NORM(V) \
-  hipLaunchKernelGGL((block_norm_backward_kernel<XF, BF, WF, V>), dim3(a.groups), dim3(norm_threads<V>(a.H)), 0, s, a)
-  if (a.H <= 8192) TPF_NORM(1);
-  else if (a.H <= 16384) TPF_NORM(2);
-  else TPF_NORM(4);
+#define TPF_NORM(V)                                                                                         \
+  if (norm_streams<XF>(a))                                                                                  \
+    hipLaunchKernelGGL((block_norm_backward_kernel<XF, BF, WF, V, 1>), dim3(a.groups),                      \
+                       dim3(norm_threads<V>(a.H)), 0, s, a);                                                \
+  else                                                                                                      \
+    hipLaunchKernelGGL((block_norm_backward_kernel<XF, BF, WF, V, 0>), dim3(a.groups),                      \
+                       dim3(norm_threads<V>(a.H)), 0, s, a)
+  if (a.H <= 8192) {
+    TPF_NORM(1);
+  } else if (a.H <= 16384) {
+    TPF_NORM(2);
+  } else {
+    TPF_NORM(4);
+  }
 #undef TPF_NORM
 }
 

@@ -11,6 +11,17 @@
 
 namespace tpf {
 
+template <int STREAM, class V>
+__device__ __forceinline__ void put(V* p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+template <int STREAM, class V>
+__device__ __forceinline__ V get(const V* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+
 typedef u32x2_t u32x2a4_t __attribute__((aligned(4)));   // codes rows are 8-byte aligned at least
 
 template <class A>
@@ -50,8 +61,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // One wave packs 32 rows x 128 columns: lane l holds the eight columns
 // 8 (l % 16) of rows l / 16 + 4 i, so a 32-column block is four lanes wide and
-// its largest value takes the lane's own maximum and four exchanges.
-template <int GELU>
+// its largest value takes the lane's own maximum and four exchanges.  u is read
+// for the last time and the codes not before the backward pass, so both go past
+// the caches.  Bound by memory: 4 x 4096 x 4096 with GeLU in 64 us, 5.25 TB/s, a
+// large copy's rate and more (73 us with u and the codes through the caches).
+template <int GELU, int STREAM>
 __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
   (void)args;
   const StashArgs& a = stash_kernarg<StashArgs>();
@@ -73,7 +87,7 @@ __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
   for (int i = 0; i < 8; ++i) {
     const int row = row0 + 4 * i;
     w[i] = u32x4_t{0, 0, 0, 0};
-    if (cok && row < a.M) w[i] = *reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.F + col);
+    if (cok && row < a.M) w[i] = get<1>(reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.F + col));
   }
   // Largest finite magnitude, as bf16 bits.
   uint32_t top = 0;
@@ -109,23 +123,29 @@ __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
       if constexpr (GELU) hv[j] = pack_bf16(lo * gauss(lo).cdf, hi * gauss(hi).cdf);
     }
     const int64_t at = (int64_t)row * a.F + col;
-    *reinterpret_cast<u32x2a4_t*>(a.codes[k] + at) = c;
-    if constexpr (GELU) *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.h[k]) + at) = hv;
+    put<1>(reinterpret_cast<u32x2_t*>(a.codes[k] + at), c);
+    if constexpr (GELU) put<STREAM>(reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.h[k]) + at), hv);
   }
   if (cok && (lane & 51) == 0) a.scales[k][(int64_t)band * nsc + (col >> 5)] = (uint8_t)e;
 }
 
-hipError_t launch_stash_pack(const StashArgs& a, int gelu, int num_cus, hipStream_t s) {
-  (void)num_cus;
+template <int STREAM>
+static void launch_pack(const StashArgs& a, int gelu, dim3 grid, hipStream_t s) {
+  if (gelu) hipLaunchKernelGGL((stash_pack_kernel<1, STREAM>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((stash_pack_kernel<0, STREAM>), grid, dim3(256), 0, s, a);
+}
+
+hipError_t launch_stash_pack(const StashArgs& a, int gelu, hipStream_t s) {
   const int64_t units = (int64_t)((a.F + 127) / 128) * ((a.M + 31) / 32) * a.p;
   const dim3 grid((unsigned)((units + 3) / 4));
-  if (gelu) hipLaunchKernelGGL(stash_pack_kernel<1>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(stash_pack_kernel<0>, grid, dim3(256), 0, s, a);
+  if ((int64_t)a.p * a.M * a.F * (gelu ? 3 : 1) >= kStreamBytes) launch_pack<1>(a, gelu, grid, s);
+  else launch_pack<0>(a, gelu, grid, s);
   return hipGetLastError();
 }
 
 // du = dh (Phi(u) + u phi(u)) and h = u Phi(u) from the stored values, eight
-// columns a lane.
+// columns a lane.  Bound by memory: 8 x 2048 x 6144 in 121 us, 5.8 TB/s.
+template <int STREAM>
 __global__ __launch_bounds__(256) void stash_backward_kernel(StashArgs args) {
   (void)args;
   const StashArgs& a = stash_kernarg<StashArgs>();
@@ -140,7 +160,7 @@ __global__ __launch_bounds__(256) void stash_backward_kernel(StashArgs args) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int row = (int)(i / fv), v = (int)(i - (int64_t)row * fv);
     const u32x2_t c = *reinterpret_cast<const u32x2a4_t*>(codes + i * 8);
-    const u32x4_t g = *reinterpret_cast<const u32x4_t*>(dh + i * 8);
+    const u32x4_t g = get<STREAM>(reinterpret_cast<const u32x4_t*>(dh + i * 8));
     const float scale = __uint_as_float((uint32_t)scales[(int64_t)(row >> 5) * nsc + (v >> 2)] << 23);
     u32x4_t o, y;
 #pragma unroll
@@ -155,15 +175,17 @@ __global__ __launch_bounds__(256) void stash_backward_kernel(StashArgs args) {
       o[j] = pack_bf16(d0, d1);
       y[j] = pack_bf16(u0 * g0.cdf, u1 * g1.cdf);
     }
-    *reinterpret_cast<u32x4_t*>(du + i * 8) = o;
-    *reinterpret_cast<u32x4_t*>(h + i * 8) = y;
+    put<STREAM>(reinterpret_cast<u32x4_t*>(du + i * 8), o);
+    put<STREAM>(reinterpret_cast<u32x4_t*>(h + i * 8), y);
   }
 }
 
 hipError_t launch_stash_backward(const StashArgs& a, int num_cus, hipStream_t s) {
   const int64_t groups = ((int64_t)a.M * (a.F / 8) + 255) / 256;
   const int64_t cap = std::max<int64_t>(1, (int64_t)num_cus * 32 / a.p);
-  hipLaunchKernelGGL(stash_backward_kernel, dim3((unsigned)std::min(groups, cap), (unsigned)a.p), dim3(256), 0, s, a);
+  const dim3 grid((unsigned)std::min(groups, cap), (unsigned)a.p);
+  if ((int64_t)a.p * a.M * a.F * 4 >= kStreamBytes) hipLaunchKernelGGL(stash_backward_kernel<1>, grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(stash_backward_kernel<0>, grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
