@@ -87,6 +87,25 @@ PyObject* operands(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return result;
 }
 
+// A tuple of whole numbers.
+bool sizes_of(PyObject* shape, std::vector<int64_t>& dims) {
+  if (!PyTuple_Check(shape)) {
+    PyErr_SetString(PyExc_TypeError, "expected a tuple of sizes");
+    return false;
+  }
+  for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(shape); ++i) {
+    dims.push_back(PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i)));
+    if (dims.back() == -1 && PyErr_Occurred()) return false;
+  }
+  return true;
+}
+
+at::Tensor new_tensor(PyObject* dtype, const std::vector<int64_t>& dims, long device) {
+  return at::empty(dims, at::TensorOptions()
+                             .dtype(reinterpret_cast<THPDtype*>(dtype)->scalar_type)
+                             .device(at::Device(at::kCUDA, (at::DeviceIndex)device)));
+}
+
 // empty(device, dtype, shape, dtype, shape, ...): new tensors on the GPU, in a
 // tuple; None for a shape of None.
 PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -100,29 +119,16 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (!result) return nullptr;
   try {
     for (Py_ssize_t g = 0; g < n / 2; ++g) {
-      PyObject *dtype = args[1 + 2 * g], *shape = args[2 + 2 * g];
+      PyObject *dtype = args[1 + 2 * g], *shape = args[2 + 2 * g], *o = nullptr;
+      std::vector<int64_t> dims;
       if (shape == Py_None) {
         Py_INCREF(Py_None);
-        PyTuple_SET_ITEM(result, g, Py_None);
-        continue;
+        o = Py_None;
+      } else if (!THPDtype_Check(dtype)) {
+        PyErr_SetString(PyExc_TypeError, "empty: expected a dtype");
+      } else if (sizes_of(shape, dims)) {
+        o = THPVariable_Wrap(new_tensor(dtype, dims, device));
       }
-      if (!THPDtype_Check(dtype) || !PyTuple_Check(shape)) {
-        PyErr_SetString(PyExc_TypeError, "empty: expected a dtype and a tuple");
-        Py_DECREF(result);
-        return nullptr;
-      }
-      std::vector<int64_t> dims(PyTuple_GET_SIZE(shape));
-      for (size_t i = 0; i < dims.size(); ++i) {
-        dims[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
-        if (dims[i] == -1 && PyErr_Occurred()) {
-          Py_DECREF(result);
-          return nullptr;
-        }
-      }
-      at::Tensor t = at::empty(dims, at::TensorOptions()
-                                         .dtype(reinterpret_cast<THPDtype*>(dtype)->scalar_type)
-                                         .device(at::Device(at::kCUDA, (at::DeviceIndex)device)));
-      PyObject* o = THPVariable_Wrap(std::move(t));
       if (!o) {
         Py_DECREF(result);
         return nullptr;
@@ -137,11 +143,62 @@ PyObject* empty(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return result;
 }
 
+// shards(device, p, dtype, shape, ...): for each group p new tensors of that
+// shape, one after the other in one allocation, and their addresses as bytes:
+// (tensors, bytes, tensors, bytes, ...).
+PyObject* shards(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (n < 2 || n % 2 != 0) {
+    PyErr_SetString(PyExc_TypeError, "shards(device, p, dtype, shape, ...)");
+    return nullptr;
+  }
+  const long device = PyLong_AsLong(args[0]), p = PyLong_AsLong(args[1]);
+  if (PyErr_Occurred()) return nullptr;
+  PyObject* result = PyTuple_New(n - 2);
+  if (!result) return nullptr;
+  try {
+    for (Py_ssize_t g = 2; g < n; g += 2) {
+      std::vector<int64_t> dims{p};
+      if (!THPDtype_Check(args[g]) || !sizes_of(args[g + 1], dims)) {
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_TypeError, "shards: expected a dtype");
+        Py_DECREF(result);
+        return nullptr;
+      }
+      const at::Tensor all = new_tensor(args[g], dims, device);
+      PyObject* bytes = PyBytes_FromStringAndSize(nullptr, p * (Py_ssize_t)sizeof(void*));
+      PyObject* tensors = PyTuple_New(p);
+      PyTuple_SET_ITEM(result, g - 2, tensors);   // held by `result` from here on
+      PyTuple_SET_ITEM(result, g - 1, bytes);
+      if (!bytes || !tensors) {
+        Py_DECREF(result);
+        return nullptr;
+      }
+      void** to = reinterpret_cast<void**>(PyBytes_AS_STRING(bytes));
+      for (long k = 0; k < p; ++k) {
+        at::Tensor t = all.select(0, k);
+        to[k] = t.data_ptr();
+        PyObject* o = THPVariable_Wrap(std::move(t));
+        if (!o) {
+          Py_DECREF(result);
+          return nullptr;
+        }
+        PyTuple_SET_ITEM(tensors, k, o);
+      }
+    }
+  } catch (...) {
+    Py_DECREF(result);
+    torch::translate_exception_to_python(std::current_exception());
+    return nullptr;
+  }
+  return result;
+}
+
 PyMethodDef methods[] = {
     {"operands", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(operands)), METH_FASTCALL,
      "operands(device, tensors, dtype, shape, ...): addresses of each group's tensors, or None"},
     {"empty", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(empty)), METH_FASTCALL,
      "empty(device, dtype, shape, ...): new tensors on the GPU"},
+    {"shards", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(shards)), METH_FASTCALL,
+     "shards(device, p, dtype, shape, ...): p new tensors of each shape, and their addresses"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_args", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -586,6 +586,13 @@ def _empty(dev, *groups):
     return _args.empty(dev.index, *groups)
 
 
+def _shards(dev, p: int, *groups):
+    """p new tensors and their addresses for each (dtype, shape): (tensors, addresses, ...)."""
+    if _args is None:
+        load()
+    return _args.shards(dev.index, p, *groups)
+
+
 def _norm_operands(x, blocks, w_pre, w_post, gate):
     """Checks shared by the norm's two directions; returns (device, M, H, gate kind, the
     blocks' addresses)."""
@@ -699,12 +706,10 @@ def stash_pack(u: Sequence[torch.Tensor], gelu: bool = True, handle: Optional[Ha
         _check("u", u, (M, F))
         at = (_ptrs(u),)
     with _on(stream):
-        new = _empty(dev, *((torch.float8_e4m3fn, (M, F)) * p + (torch.uint8, _stash_shape(M, F)) * p
-                            + (torch.bfloat16, (M, F)) * (p if gelu else 0)))
-    codes, scales, h = new[:p], new[p:2 * p], new[2 * p:] if gelu else None
+        codes, cat, scales, sat = _shards(dev, p, torch.float8_e4m3fn, (M, F), torch.uint8, _stash_shape(M, F))
+        h, hat = _shards(dev, p, torch.bfloat16, (M, F)) if gelu else (None, None)
     hd, sp = _ctx(handle, dev, stream)
-    check(load().tpf_stash_pack(hd, p, M, F, at[0], 1 if gelu else 0, _ptrs(h) if gelu else None,
-                                _ptrs(codes), _ptrs(scales), sp))
+    check(load().tpf_stash_pack(hd, p, M, F, at[0], 1 if gelu else 0, hat, cat, sat, sp))
     return h, codes, scales
 
 
@@ -736,11 +741,9 @@ def stash_backward(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tensor]
         _check("dh", dh, (M, F), device=dev)
         dat = (_ptrs(dh),)
     with _on(stream):
-        new = _empty(dev, *((torch.bfloat16, (M, F)) * (2 * p)))
-    du, h = new[:p], new[p:]
+        du, uat, h, hat = _shards(dev, p, torch.bfloat16, (M, F), torch.bfloat16, (M, F))
     hd, sp = _ctx(handle, dev, stream)
-    check(load().tpf_stash_backward(hd, p, M, F, *at, dat[0], _ptrs(du), _ptrs(h),
-                                    sp))
+    check(load().tpf_stash_backward(hd, p, M, F, *at, dat[0], uat, hat, sp))
     return du, h
 
 
@@ -759,18 +762,20 @@ def stash_weight_grad(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tens
     if dW is None:
         _need(out_dtype in OUT_DTYPES, f"output dtype must be bfloat16 or float32, got {out_dtype}")
         with _on(stream):
-            dW = list(_empty(dev, *((out_dtype, (R, C)) * p)))
+            dW, wat = _shards(dev, p, out_dtype, (R, C))
+            dW = list(dW)
     else:
         _check_shards("dW", dW, p)
         _check("dW", dW, (R, C), OUT_DTYPES, dev)
         _need(all(d.dtype == dW[0].dtype for d in dW), "dW: the shards differ in dtype")
+        wat = _ptrs(dW)
     _check_ws(ws, dev)
     need = load().tpf_stash_weight_grad_ws(p, M, R, C)
     if ws is None and need:
         with _on(stream):
             ws, = _empty(dev, torch.uint8, (need,))
     hd, sp = _ctx(handle, dev, stream)
-    check(load().tpf_stash_weight_grad(hd, p, M, R, C, *at, yat[0], _ptrs(dW),
+    check(load().tpf_stash_weight_grad(hd, p, M, R, C, *at, yat[0], wat,
                                        _dtype_code(dW[0].dtype), ws.data_ptr() if ws is not None else None,
                                        ws.numel() * ws.element_size() if ws is not None else 0, sp))
     return dW
