@@ -129,17 +129,12 @@ __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
   if (cok && (lane & 51) == 0) a.scales[k][(int64_t)band * nsc + (col >> 5)] = (uint8_t)e;
 }
 
-template <int STREAM>
-static void launch_pack(const StashArgs& a, int gelu, dim3 grid, hipStream_t s) {
-  if (gelu) hipLaunchKernelGGL((stash_pack_kernel<1, STREAM>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((stash_pack_kernel<0, STREAM>), grid, dim3(256), 0, s, a);
-}
-
 hipError_t launch_stash_pack(const StashArgs& a, int gelu, hipStream_t s) {
   const int64_t units = (int64_t)((a.F + 127) / 128) * ((a.M + 31) / 32) * a.p;
   const dim3 grid((unsigned)((units + 3) / 4));
-  if ((int64_t)a.p * a.M * a.F * (gelu ? 3 : 1) >= kStreamBytes) launch_pack<1>(a, gelu, grid, s);
-  else launch_pack<0>(a, gelu, grid, s);
+  if (!gelu) hipLaunchKernelGGL((stash_pack_kernel<0, 0>), grid, dim3(256), 0, s, a);
+  else if ((int64_t)a.p * a.M * a.F * 2 >= kStreamBytes) hipLaunchKernelGGL((stash_pack_kernel<1, 1>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((stash_pack_kernel<1, 0>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
