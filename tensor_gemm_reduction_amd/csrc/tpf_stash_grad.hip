@@ -10,6 +10,12 @@
 // The smaller A tile leaves LDS for three slots of both operands: the loads of
 // step t + 2 go out between the MFMAs of step t's first three slices, one or
 // two at a time, into the slot that step t - 1 left.
+//
+// 4 shards of 4096^3: 435 us, 1263 TFLOP/s, what a large library product of bf16
+// reaches on the card (1264): bound by the matrix cores at the clock they are held
+// to.  2 x [1003, 1352 x 2056]: 20.7 us (540 TFLOP/s): 374 tiles of 128 x 128 leave
+// 138 of 256 compute units with one tile and 118 with two, 0.8 us a step of 64 rows,
+// and about 10 us go to the start, the first loads and the stores.
 #include <algorithm>
 
 #include "tpf_block.hpp"
