@@ -187,10 +187,13 @@ struct ScaleStream {
     left -= kBlockUnits;
   }
   // Leaves the loaded block in `lds` for its wave; `eight` is the zero point of
-  // weights that have none.
+  // weights that have none.  A wave's LDS accesses are carried out in order, so
+  // its lanes need no barrier between them, only the compiler's order.
   __device__ __forceinline__ void publish(uint32_t* lds, uint32_t eight, int lane) const {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int e = 0; e < EACH; ++e) lds[(lane % GB) * PITCH + (e * 64 + lane) / GB] = (s[e] << 16) | z[e] | eight;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 };
 

@@ -13,9 +13,10 @@
 //
 // 4 shards of 4096^3: 435 us, 1263 TFLOP/s, what a large library product of bf16
 // reaches on the card (1264): bound by the matrix cores at the clock they are held
-// to.  2 x [1003, 1352 x 2056]: 20.7 us (540 TFLOP/s): 374 tiles of 128 x 128 leave
+// to.  2 x [1003, 1352 x 2056]: 19.7 us (566 TFLOP/s): 374 tiles of 128 x 128 leave
 // 138 of 256 compute units with one tile and 118 with two, 0.8 us a step of 64 rows,
-// and about 10 us go to the start, the first loads and the stores.
+// and about 8 us go to the start, the first loads and the stores (10 with two-byte
+// stores).
 #include <algorithm>
 
 #include "tpf_block.hpp"
@@ -184,6 +185,36 @@ __device__ __forceinline__ void sg_step(Frag<Cfg>& f, SgSlice<Cfg> (&d)[2], uint
   sg_mfma<Cfg, 0, 0>(f, d[1], w1, ld, fq, fb, 0);
 }
 
+// store_tile for bf16, two columns a store: neighbouring lanes hold neighbouring
+// columns and exchange one of two rows, so that the even lane stores the first
+// row and the odd lane the second.  C is even, so both columns are inside or not.
+template <class Cfg>
+__device__ __forceinline__ void store_tile_bf16(const Frag<Cfg>& f, const TileJob& j, void* out, int64_t ldo) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+  const bool odd = lane & 1;
+  const auto rs = make_rsrc(reinterpret_cast<char*>(out) + ((int64_t)j.m0 * ldo + j.n0) * 2, (int64_t)j.rows * ldo * 2);
+  const int pitch = __builtin_amdgcn_readfirstlane((int)ldo * 2);
+#pragma unroll
+  for (int i = 0; i < Cfg::TM; ++i) {
+#pragma unroll
+    for (int jn = 0; jn < Cfg::TN; ++jn) {
+      const int col = wn * Cfg::WN + jn * 32 + (lane & 30);
+      const int row0 = wm * Cfg::WM + i * 32 + 4 * (lane >> 5) + odd;
+#pragma unroll
+      for (int v = 0; v < 16; v += 2) {
+        const float a = f.acc[i][jn][v], b = f.acc[i][jn][v + 1];
+        const float other = __int_as_float(
+            __builtin_amdgcn_mov_dpp(__float_as_int(odd ? a : b), 0xB1, 0xf, 0xf, true));   // lanes 2 n and 2 n + 1
+        const bf16x2_t two = {(__bf16)(odd ? other : a), (__bf16)(odd ? b : other)};
+        const int row = row0 + 8 * (v >> 2) + (v & 3);
+        const int off = row < j.rows && j.n0 + col < j.N ? row * pitch + col * 2 : (int)kOOB;
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, two), rs, off, 0, 0);
+      }
+    }
+  }
+}
+
 template <class Cfg>
 __global__ __launch_bounds__(Cfg::THREADS) void stash_grad_kernel(StashGradArgs args) {
   (void)args;
@@ -247,7 +278,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void stash_grad_kernel(StashGradArgs 
   else if (a.out == OUT_F32)
     store_tile<Cfg, OUT_F32>(f, j, a.dW[k], a.C);
   else
-    store_tile<Cfg, OUT_BF16>(f, j, a.dW[k], a.C);
+    store_tile_bf16<Cfg>(f, j, a.dW[k], a.C);
 }
 
 // The parts of a cut contraction, added in order, four elements a thread.
