@@ -68,7 +68,7 @@ def _args_command(out: str):
     return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
              os.path.join(CSRC, "tpf_args.cpp"), "-o", out] + [f"-I{i}" for i in include]
-            + ["-L" + cpp_extension.TORCH_LIB_PATH, "-ltorch_python", "-ltorch_cpu", "-lc10"])
+            + ["-L" + cpp_extension.TORCH_LIB_PATH, "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10"])
 
 
 def build(verbose: bool = False) -> str:

@@ -12,7 +12,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 
 #include <exception>
 #include <vector>
@@ -101,9 +101,8 @@ bool sizes_of(PyObject* shape, std::vector<int64_t>& dims) {
 }
 
 at::Tensor new_tensor(PyObject* dtype, const std::vector<int64_t>& dims, long device) {
-  return at::empty(dims, at::TensorOptions()
-                             .dtype(reinterpret_cast<THPDtype*>(dtype)->scalar_type)
-                             .device(at::Device(at::kCUDA, (at::DeviceIndex)device)));
+  return at::Tensor(at::detail::empty_cuda(dims, reinterpret_cast<THPDtype*>(dtype)->scalar_type,
+                                           at::Device(at::kCUDA, (at::DeviceIndex)device), std::nullopt));
 }
 
 // empty(device, dtype, shape, dtype, shape, ...): new tensors on the GPU, in a
