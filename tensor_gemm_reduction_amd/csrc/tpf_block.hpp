@@ -48,6 +48,7 @@ struct NormArgs {
   int gate_kind;
   float alpha, beta, eps, offset;    // offset: 1 where the weights are stored as offsets from 1
   int groups;                        // backward: workgroups, each summing rows group, group + groups, ...
+  uint32_t row0;                     // forward: the launch's first row
 };
 
 // Workgroups of the backward's row pass: a pure function of M and H.

@@ -149,8 +149,8 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs args) {
   const NormArgs& a = norm_kernarg<NormArgs>();
   __shared__ float lds[2][1][16];
   const int T = blockDim.x, t = threadIdx.x, waves = T / 64, wave = t >> 6;
-  const int m = blockIdx.x * blockDim.y + threadIdx.y;
-  if (m >= a.M) return;      // only where a row is one wave: no barrier follows
+  const uint32_t m = a.row0 + blockIdx.x * blockDim.y + threadIdx.y;
+  if (m >= (uint32_t)a.M) return;      // only where a row is one wave: no barrier follows
   const int64_t row = (int64_t)m * a.H;
   F8 b[V];
   Raw8<XF> xr[V];
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs args) {
   }
   if (a.stats && t == 0) {
     a.stats[m] = rb;
-    a.stats[a.M + m] = rx;
+    a.stats[a.M + (int64_t)m] = rx;
   }
 }
 
@@ -252,19 +252,19 @@ __global__ __launch_bounds__(1024) void block_norm_backward_kernel(NormArgs args
     Raw8<0> dy[V];
     float rb, rx, g;
   };
-  auto load_part = [&](Row& r, int m, int i) {
+  auto load_part = [&](Row& r, uint32_t m, int i) {
     const int64_t at = (int64_t)m * a.H + (i * T + t) * 8;
     r.b[i] = load_raw<BF>(a.blocks[0], at);
     r.x[i] = load_raw<XF>(a.x, at);
     r.dy[i] = load_raw<0>(a.dy, at);
     if (a.dx_out) r.e[i] = load_raw<XF>(a.dx_out, at);
   };
-  auto load_row = [&](Row& r, int m) {
+  auto load_row = [&](Row& r, uint32_t m) {
     if constexpr (HOLD) {
       if (t * 8 < a.H) load_part(r, m, 0);
     }
     r.rb = a.stats[m];
-    r.rx = a.stats[a.M + m];
+    r.rx = a.stats[a.M + (int64_t)m];
     r.g = a.gate_kind == GATE_TOKEN ? load1_any(a.gate, m, a.w_f32) : 1.0f;
   };
   const bool channel = a.gate_kind == GATE_CHANNEL;
@@ -303,10 +303,11 @@ __global__ __launch_bounds__(1024) void block_norm_backward_kernel(NormArgs args
   int par = 0;
   Row next;
   load_row(next, blockIdx.x);
-  for (int m = blockIdx.x; m < a.M; m += a.groups, par ^= 1) {
+  // Row numbers are unsigned: the last one plus `groups` can pass 31 bits.
+  for (uint32_t m = blockIdx.x; m < (uint32_t)a.M; m += a.groups, par ^= 1) {
     const int64_t row = (int64_t)m * a.H;
     Row r = next;
-    if (m + a.groups < a.M) load_row(next, m + a.groups);
+    if (m + a.groups < (uint32_t)a.M) load_row(next, m + a.groups);
     F8 bh, xh, e;
     float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -427,9 +428,14 @@ static bool norm_streams(const NormArgs& a) {
 template <int XF, int BF, int V>
 static void launch_norm_v(const NormArgs& a, hipStream_t s) {
   const int T = norm_threads<V>(a.H), rows = T == 64 ? kNormRows : 1;
-  const dim3 grid((a.M + rows - 1) / rows), block(T, rows);
-  if (norm_streams<XF>(a)) hipLaunchKernelGGL((block_norm_kernel<XF, BF, V, 1>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((block_norm_kernel<XF, BF, V, 0>), grid, block, 0, s, a);
+  const int64_t most = UINT32_MAX / T, groups = ((int64_t)a.M + rows - 1) / rows;   // a grid has fewer than 2^32 threads
+  for (int64_t g = 0; g < groups; g += most) {
+    NormArgs part = a;
+    part.row0 = (uint32_t)(g * rows);
+    const dim3 grid((unsigned)std::min(groups - g, most)), block(T, rows);
+    if (norm_streams<XF>(a)) hipLaunchKernelGGL((block_norm_kernel<XF, BF, V, 1>), grid, block, 0, s, part);
+    else hipLaunchKernelGGL((block_norm_kernel<XF, BF, V, 0>), grid, block, 0, s, part);
+  }
 }
 
 template <int XF, int BF>
