@@ -68,6 +68,7 @@ struct StashArgs {
   uint8_t* scales[kMaxShards];
   const void* dh[kMaxShards];        // backward: [M][F] bf16
   void* du[kMaxShards];              // backward: [M][F] bf16
+  int64_t unit0;                     // pack: the launch's first unit of 32 x 128
   int p, M, F;
 };
 hipError_t launch_stash_pack(const StashArgs& a, int gelu, hipStream_t s);

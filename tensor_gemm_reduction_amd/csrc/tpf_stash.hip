@@ -70,24 +70,25 @@ __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
   (void)args;
   const StashArgs& a = stash_kernarg<StashArgs>();
   const int lane = threadIdx.x & 63;
-  const int strips = (a.F + 127) / 128, bands = (a.M + 31) / 32;
+  const uint32_t rows = a.M;      // unsigned: a band's last row can be past 31 bits
+  const int strips = (a.F + 127) / 128, bands = (int)((rows + 31) / 32);
   const int nsc = (a.F + 31) / 32;
   const int64_t units = (int64_t)strips * bands;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t unit = a.unit0 + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (unit >= units * a.p) return;
   const int k = __builtin_amdgcn_readfirstlane((int)(unit / units));
   const int64_t r = unit - k * units;
   const int band = (int)(r / strips), strip = (int)(r % strips);
   const int col = strip * 128 + (lane & 15) * 8;
-  const int row0 = band * 32 + (lane >> 4);
+  const uint32_t row0 = (uint32_t)band * 32 + (lane >> 4);
   const uint16_t* u = reinterpret_cast<const uint16_t*>(a.u[k]);
   const bool cok = col < a.F;
   u32x4_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = row0 + 4 * i;
+    const uint32_t row = row0 + 4 * i;
     w[i] = u32x4_t{0, 0, 0, 0};
-    if (cok && row < a.M) w[i] = get<1>(reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.F + col));
+    if (cok && row < rows) w[i] = get<1>(reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.F + col));
   }
   // Largest finite magnitude, as bf16 bits.
   uint32_t top = 0;
@@ -108,8 +109,8 @@ __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
   const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = row0 + 4 * i;
-    if (!cok || row >= a.M) continue;
+    const uint32_t row = row0 + 4 * i;
+    if (!cok || row >= rows) continue;
     u32x2_t c;
     u32x4_t hv;
 #pragma unroll
@@ -130,11 +131,16 @@ __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
 }
 
 hipError_t launch_stash_pack(const StashArgs& a, int gelu, hipStream_t s) {
-  const int64_t units = (int64_t)((a.F + 127) / 128) * ((a.M + 31) / 32) * a.p;
-  const dim3 grid((unsigned)((units + 3) / 4));
-  if (!gelu) hipLaunchKernelGGL((stash_pack_kernel<0, 0>), grid, dim3(256), 0, s, a);
-  else if ((int64_t)a.p * a.M * a.F * 2 >= kStreamBytes) hipLaunchKernelGGL((stash_pack_kernel<1, 1>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((stash_pack_kernel<1, 0>), grid, dim3(256), 0, s, a);
+  const int64_t units = (int64_t)((a.F + 127) / 128) * (((int64_t)a.M + 31) / 32) * a.p;
+  const int64_t most = (int64_t)UINT32_MAX / 256 * 4;      // a grid has fewer than 2^32 threads
+  for (int64_t u = 0; u < units; u += most) {
+    StashArgs part = a;
+    part.unit0 = u;
+    const dim3 grid((unsigned)((std::min(units - u, most) + 3) / 4));
+    if (!gelu) hipLaunchKernelGGL((stash_pack_kernel<0, 0>), grid, dim3(256), 0, s, part);
+    else if ((int64_t)a.p * a.M * a.F * 2 >= kStreamBytes) hipLaunchKernelGGL((stash_pack_kernel<1, 1>), grid, dim3(256), 0, s, part);
+    else hipLaunchKernelGGL((stash_pack_kernel<1, 0>), grid, dim3(256), 0, s, part);
+  }
   return hipGetLastError();
 }
 

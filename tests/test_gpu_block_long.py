@@ -68,3 +68,25 @@ def test_norm_of_the_most_rows():
     v = 0.7 * rx * (u + xh * (u * xh).mean(1, keepdim=True))
     for got, ref, size in ((dw_pre, want[2], d.abs() * xh), (dw_post, want[3], v * bh)):
         assert ((got - ref).abs().double() <= 2 * len(ROWS) * 2.0 ** -24 * size.sum(0)).all()
+
+
+def test_stash_of_the_most_rows():
+    at = torch.tensor(ROWS, device="cuda")
+    u, rows = sparse(at, 3)
+    rows[::7] *= 300                        # blocks of different factors
+    u[at] = rows
+    _, (codes,), (scales,) = tp.stash_pack([u], gelu=False)
+    du, h = (t[0] for t in tp.stash_backward([codes], [scales], [u]))
+    # the blocks of 32 rows that hold values, by themselves
+    bands = torch.unique(at // 32)
+    take = (bands[:, None] * 32 + torch.arange(32, device="cuda")).view(-1)
+    take = take[take < M]
+    _, (want,), (byte,) = tp.stash_pack([u[take]], gelu=False)
+    want_du, want_h = (t[0] for t in tp.stash_backward([want], [byte], [u[take]]))
+    del u
+    assert torch.equal(scales[bands], byte)
+    scales[bands] = 10
+    assert bool((scales == 10).all())       # nothing but zeros: the least factor
+    same(du, take, want_du)
+    same(h, take, want_h)
+    same(codes.view(torch.uint8), take, want.view(torch.uint8))
