@@ -363,15 +363,17 @@ int tpf_block_norm_backward(tpf_handle h, int p, int64_t M, int64_t H, const voi
  * e a block, the factor 2^(e-127): the least one, not below 2^-117, that keeps
  * the block's largest finite magnitude within 448 of it.  codes[k] [M, F] are
  * OCP e4m3 values of u 2^(127-e), rounded to nearest even, and NaN where u is
- * not finite.  With gelu != 0 the same pass writes h[k] [M, F] bf16 =
- * GeLU(u) (erf form, fp32, rounded once); otherwise h is ignored.
+ * not finite.  With gelu != 0 the same pass writes act[k] [M, F] bf16 =
+ * GeLU(u) (erf form, in fp32 to 2^-16 of the value, rounded once); otherwise
+ * act is ignored.
  * F must be a multiple of 8; codes are 8-byte aligned, scales any byte. */
 int tpf_stash_pack(tpf_handle h, int p, int64_t M, int64_t F, const void* const* u, int gelu, void* const* act,
                    void* const* codes, void* const* scales, void* stream);
 
 /* GeLU's gradient from the 8-bit activations: with u = code * 2^(e-127) and
  * Phi, phi the normal distribution and density,
- *   du[k] = dh[k] (Phi(u) + u phi(u)),  act[k] = u Phi(u)      bf16, [M, F]. */
+ *   du[k] = dh[k] (Phi(u) + u phi(u)),  act[k] = u Phi(u)      bf16, [M, F],
+ * each evaluated in fp32 and rounded once. */
 int tpf_stash_backward(tpf_handle h, int p, int64_t M, int64_t F, const void* const* codes,
                        const void* const* scales, const void* const* dh, void* const* du, void* const* act,
                        void* stream);
