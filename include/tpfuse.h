@@ -399,7 +399,8 @@ size_t tpf_stash_weight_grad_ws(int p, int64_t M, int64_t R, int64_t C);
  *   Y: [M, N] of y_dtype; with gelu != 0 GeLU of the fp32 sum.
  * group is 32, 64 or 128 and divides K; N is any positive number.  Weights are
  * read once for every 64 rows of X.  Sums are fp32, in an order fixed by the
- * sizes.  scales need 2-byte alignment, zeros none. */
+ * sizes.  Infinities and NaN in X reach Y as in that sum; a call that has them
+ * takes up to milliseconds.  scales need 2-byte alignment, zeros none. */
 int tpf_qweight_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, int group, const void* const* X,
                        const void* const* codes, const void* const* scales, const void* const* zeros, int gelu,
                        void* Y, int y_dtype, void* ws, size_t ws_bytes, void* stream);
