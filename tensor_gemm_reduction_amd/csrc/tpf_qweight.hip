@@ -220,8 +220,8 @@ __device__ __forceinline__ bf16x8_t bf16_ones() {
 }
 // One element over units u0 .. u1 - 1 by the definition; (q - z) s is exact in
 // fp32.  Rare and bound by latency: one infinity in 16 rows over 8 shards of 1024
-makes 22 us 290; a NaN at the end of each of 64 rows over 8 of 3584 makes 69 us
-5.8 ms.
+// makes 22 us 290; a NaN at the end of each of 64 rows over 8 of 3584 makes 69 us
+// 5.8 ms.
 __device__ __forceinline__ float qw_term_by_term(const QweightArgs& a, int m, int n, int u0, int u1) {
   const int per = (a.K + 127) / 128, gps = a.K / a.group;
   float y = 0.0f;
