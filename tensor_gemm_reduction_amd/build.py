@@ -71,25 +71,40 @@ def _args_command(out: str):
             + ["-L" + cpp_extension.TORCH_LIB_PATH, "-ltorch_python", "-ltorch_hip", "-ltorch_cpu", "-lc10"])
 
 
+def _start(name: str, cmd, verbose: bool):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+
+
+def _failure(name: str, pr, verbose: bool):
+    """What a finished compiler said if it failed, else None."""
+    out, err = pr.communicate()
+    if pr.returncode != 0:
+        return f"compiling {name} failed:\n{out}\n{err}"
+    if verbose and err.strip():
+        print(err, file=sys.stderr)
+    return None
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source for gfx950, link libtpfuse.so and the binding's
-    argument checks; returns the library's path."""
+    argument checks; returns the library's path.  The checks need g++ and
+    torch's headers: where they do not build, the library is there all the same
+    when the error is raised."""
     os.makedirs(LIBDIR, exist_ok=True)
     cc = hipcc()
     t0 = time.time()
     jobs = _compile_jobs(cc)
-    procs = []
-    for name, obj, cmd in jobs + [("tpf_args.cpp", ARGS, _args_command(ARGS + ".tmp"))]:
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
-    failed = []
-    for name, pr in procs:
-        out, err = pr.communicate()
-        if pr.returncode != 0:
-            failed.append(f"compiling {name} failed:\n{out}\n{err}")
-        elif verbose and err.strip():
-            print(err, file=sys.stderr)
+    procs = [_start(name, cmd, verbose) for name, _, cmd in jobs]
+    args_tmp, args_failed = ARGS + ".tmp", None
+    try:
+        args = _start("tpf_args.cpp", _args_command(args_tmp), verbose)
+    except (ImportError, OSError) as e:      # no torch, no g++
+        args, args_failed = None, f"{type(e).__name__}: {e}"
+    failed = [f for f in (_failure(name, pr, verbose) for name, pr in procs) if f]
+    if args is not None:
+        args_failed = _failure(*args, verbose)
     if failed:
         raise RuntimeError("\n".join(failed))
     objs = [obj for _, obj, _ in jobs]
@@ -99,9 +114,11 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    os.replace(ARGS + ".tmp", ARGS)
     for o in objs:
         os.remove(o)
+    if args_failed:
+        raise RuntimeError(f"{LIB} is built, but not {ARGS} (the MLP block's calls need it): {args_failed}")
+    os.replace(args_tmp, ARGS)
     if verbose:
         print(f"built {LIB} in {time.time() - t0:.1f}s", flush=True)
     return LIB
