@@ -12,8 +12,11 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <ATen/Context.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/core/TensorImpl.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 
 #include <exception>
 #include <vector>
@@ -101,9 +104,18 @@ bool sizes_of(PyObject* shape, std::vector<int64_t>& dims) {
   return true;
 }
 
+// Whether new tensors have to come through torch's dispatcher: something
+// watches or replaces its calls, or fills new memory.
+bool watched() {
+  return c10::impl::dispatch_mode_enabled() ||
+         (at::globalContext().deterministicAlgorithms() && at::globalContext().deterministicFillUninitializedMemory());
+}
+
 at::Tensor new_tensor(PyObject* dtype, const std::vector<int64_t>& dims, long device) {
-  return at::Tensor(at::detail::empty_cuda(dims, reinterpret_cast<THPDtype*>(dtype)->scalar_type,
-                                           at::Device(at::kCUDA, (at::DeviceIndex)device), std::nullopt));
+  const at::Device where(at::kCUDA, (at::DeviceIndex)device);
+  const auto type = reinterpret_cast<THPDtype*>(dtype)->scalar_type;
+  if (watched()) return at::empty(dims, at::TensorOptions().dtype(type).device(where));
+  return at::Tensor(at::detail::empty_cuda(dims, type, where, std::nullopt));
 }
 
 // Tensor k of those laid one after the other in `all` ([p, ...]): its memory,
@@ -180,7 +192,7 @@ PyObject* shards(PyObject*, PyObject* const* args, Py_ssize_t n) {
       int64_t size = (int64_t)c10::elementSize(reinterpret_cast<THPDtype*>(args[g])->scalar_type);
       for (const int64_t d : dims) size *= d;
       at::Tensor all;
-      if (p > 1 && size < kSharedBytes) {
+      if (p > 1 && size < kSharedBytes && !watched()) {
         std::vector<int64_t> together{p};
         together.insert(together.end(), dims.begin(), dims.end());
         all = new_tensor(args[g], together, device);
