@@ -602,17 +602,27 @@ def _shards(dev, p: int, *groups):
     return (_args or _native()).shards(dev.index, p, *groups)
 
 
+def _matrix(name: str, t, sizes: str):
+    """The two sizes of a matrix, the first thing that is asked of an operand."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:      # the message is built only on failure
+        _need(isinstance(t, torch.Tensor), f"{name} is not a tensor")
+        _need(False, f"{name} has {t.dim()} dimensions, expected {sizes}")
+    return t.shape
+
+
 def _norm_operands(x, blocks, w_pre, w_post, gate):
     """Checks shared by the norm's two directions; returns (device, M, H, gate kind, the
     blocks' addresses)."""
     p = len(blocks)
     _need(p >= 1, "blocks: no tensors given")
-    _need(x.dim() == 2, f"x has {x.dim()} dimensions, expected [M, H]")
-    M, H = x.shape
+    M, H = _matrix("x", x, "[M, H]")
     dev, idx = x.device, x.get_device()
-    kind = GATE_NONE if gate is None else GATE_TOKEN if gate.dim() == 2 else GATE_CHANNEL
     vec, rows = (H,), (M, H)
-    b, w = blocks[0].dtype, w_pre.dtype
+    try:
+        kind = GATE_NONE if gate is None else GATE_TOKEN if gate.dim() == 2 else GATE_CHANNEL
+        b, w = blocks[0].dtype, w_pre.dtype
+    except AttributeError:       # no tensors: named below
+        kind, b, w = GATE_CHANNEL, None, None
     if x.dtype in OUT_DTYPES and b in OUT_DTYPES and w in OUT_DTYPES:
         got = _operands(idx, blocks, b, rows, (x,), x.dtype, rows, (w_pre, w_post), w, vec,
                         () if gate is None else (gate,), w, (M, 1) if kind == GATE_TOKEN else vec)
@@ -707,8 +717,7 @@ def stash_pack(u: Sequence[torch.Tensor], gelu: bool = True, handle: Optional[Ha
     e4m3, so that u ~ codes * 2^(scales - 127)."""
     p = len(u)
     _need(p >= 1, "u: no shards given")
-    _need(u[0].dim() == 2, f"u[0] has {u[0].dim()} dimensions, expected [M, F]")
-    M, F = u[0].shape
+    M, F = _matrix("u[0]", u[0], "[M, F]")
     dev = u[0].device
     at = _operands(u[0].get_device(), u, torch.bfloat16, (M, F))
     if at is None:
@@ -725,8 +734,7 @@ def stash_pack(u: Sequence[torch.Tensor], gelu: bool = True, handle: Optional[Ha
 def _check_stash(codes, scales):
     p = len(codes)
     _need(p >= 1, "codes: no shards given")
-    _need(codes[0].dim() == 2, f"codes[0] has {codes[0].dim()} dimensions, expected [M, F]")
-    M, F = codes[0].shape
+    M, F = _matrix("codes[0]", codes[0], "[M, F]")
     _check_shards("scales", scales, p)
     dev = codes[0].device
     at = None
@@ -761,9 +769,10 @@ def stash_weight_grad(codes: Sequence[torch.Tensor], scales: Sequence[torch.Tens
                       handle: Optional[Handle] = None, stream=None) -> List[torch.Tensor]:
     """dW[k] = U_k^T dY[k], U_k [M, R] the 8-bit activations of `stash_pack`:
     `weight_grad` of an input kept in 8 bits."""
+    _need(len(dY) >= 1, "dY: no shards given")
+    _, C = _matrix("dY[0]", dY[0], "[M, C]")
     dev, p, M, R, at = _check_stash(codes, scales)
     _check_shards("dY", dY, p)
-    C = dY[0].shape[1]
     yat = _operands(dev.index, dY, torch.bfloat16, (M, C))
     if yat is None:
         _check("dY", dY, (M, C), device=dev)
@@ -803,14 +812,14 @@ def qweight_matmul(X: Sequence[torch.Tensor], codes: Sequence[torch.Tensor], sca
     W_k = (code - zero) * scale; group is 32, 64 or 128."""
     p = len(X)
     _need(p >= 1, "X: no shards given")
-    _need(X[0].dim() == 2, f"X[0] has {X[0].dim()} dimensions, expected [M, K]")
-    M, K = X[0].shape
+    M, K = _matrix("X[0]", X[0], "[M, K]")
     _need(group in (32, 64, 128) and K % group == 0, f"group {group} is not 32, 64 or 128 or does not divide K = {K}")
     _check_shards("codes", codes, p)
     _check_shards("scales", scales, p)
     if zeros is not None:
         _check_shards("zeros", zeros, p)
-    N, per_group = codes[0].shape[0], (codes[0].shape[0], K // group)
+    N, _ = _matrix("codes[0]", codes[0], "[N, K/2]")
+    per_group = N, K // group
     dev = X[0].device
     at = _operands(X[0].get_device(), X, torch.bfloat16, (M, K), codes, torch.uint8, (N, K // 2), scales, torch.bfloat16,
                    per_group, () if zeros is None else zeros, torch.uint8, per_group)
