@@ -42,15 +42,19 @@ bool addresses(PyObject* seq, PyObject* dtype, PyObject* shape, long device, PyO
   PyObject* bytes = PyBytes_FromStringAndSize(nullptr, n * (Py_ssize_t)sizeof(void*));
   bool ok = bytes != nullptr;
   void** to = ok ? reinterpret_cast<void**>(PyBytes_AS_STRING(bytes)) : nullptr;
-  for (Py_ssize_t i = 0; ok && i < n; ++i) {
-    PyObject* item = PySequence_Fast_GET_ITEM(fast, i);
-    ok = THPVariable_Check(item);
-    if (!ok) break;
-    const at::Tensor& t = THPVariable_Unpack(item);
-    ok = t.defined() && t.is_cuda() && t.get_device() == device && t.scalar_type() == type && t.dim() == dims &&
-         t.is_contiguous();
-    for (Py_ssize_t d = 0; ok && d < dims; ++d) ok = t.size(d) == want[d];
-    if (ok) to[i] = t.data_ptr();
+  try {
+    for (Py_ssize_t i = 0; ok && i < n; ++i) {
+      PyObject* item = PySequence_Fast_GET_ITEM(fast, i);
+      ok = THPVariable_Check(item);
+      if (!ok) break;
+      const at::Tensor& t = THPVariable_Unpack(item);
+      ok = t.defined() && t.is_cuda() && t.get_device() == device && t.scalar_type() == type && t.dim() == dims &&
+           t.is_contiguous();
+      for (Py_ssize_t d = 0; ok && d < dims; ++d) ok = t.size(d) == want[d];
+      if (ok) to[i] = t.data_ptr();
+    }
+  } catch (...) {   // a tensor without storage, say: not an operand
+    ok = false;
   }
   Py_DECREF(fast);
   if (!ok) {
@@ -73,20 +77,14 @@ PyObject* operands(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (device == -1 && PyErr_Occurred()) return nullptr;
   PyObject* result = PyTuple_New(n / 3);
   if (!result) return nullptr;
-  try {
-    for (Py_ssize_t g = 0; g < n / 3; ++g) {
-      PyObject* bytes = nullptr;
-      if (!addresses(args[1 + 3 * g], args[2 + 3 * g], args[3 + 3 * g], device, &bytes)) {
-        Py_DECREF(result);
-        PyErr_Clear();
-        Py_RETURN_NONE;
-      }
-      PyTuple_SET_ITEM(result, g, bytes);
+  for (Py_ssize_t g = 0; g < n / 3; ++g) {
+    PyObject* bytes = nullptr;
+    if (!addresses(args[1 + 3 * g], args[2 + 3 * g], args[3 + 3 * g], device, &bytes)) {
+      Py_DECREF(result);
+      PyErr_Clear();
+      Py_RETURN_NONE;
     }
-  } catch (const std::exception&) {   // a tensor without storage, say: not an operand
-    Py_DECREF(result);
-    PyErr_Clear();
-    Py_RETURN_NONE;
+    PyTuple_SET_ITEM(result, g, bytes);
   }
   return result;
 }
