@@ -85,10 +85,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 // One wave packs 32 rows x 128 columns: lane l holds the eight columns
 // 8 (l % 16) of rows l / 16 + 4 i, so a 32-column block is four lanes wide and
-// its largest value takes the lane's own maximum and four exchanges.  u is read
-// for the last time and the codes not before the backward pass, so both go past
-// the caches.  Bound by memory: 4 x 4096 x 4096 with GeLU in 64 us, 5.25 TB/s, a
-// large copy's rate and more (73 us with u and the codes through the caches).
+// its largest value takes the lane's own maximum and four exchanges.  The codes
+// are not read before the backward pass and go past the caches, and so does u
+// where its GeLU is what the next product reads.  Without GeLU the next products
+// read u itself: smaller than half the memory-side cache it is loaded through
+// the caches (pack of 4096 x 4096 and four products of it 365 us, past them 370),
+// larger it is not (8192 x 8192: 944 us either way, the pack alone 39 against 37).
+// Bound by memory: 4 x 4096 x 4096 with GeLU in 64 us, 5.25 TB/s, a large copy's
+// rate and more (73 us with u and the codes through the caches).
 template <int GELU, int STREAM>
 __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
   (void)args;
@@ -112,7 +116,7 @@ __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
   for (int i = 0; i < 8; ++i) {
     const uint32_t row = row0 + 4 * i;
     w[i] = u32x4_t{0, 0, 0, 0};
-    if (cok && row < rows) w[i] = get<1>(reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.F + col));
+    if (cok && row < rows) w[i] = get<GELU || STREAM>(reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.F + col));
   }
   // Largest finite magnitude, as bf16 bits.
   uint32_t top = 0;
@@ -161,8 +165,10 @@ hipError_t launch_stash_pack(const StashArgs& a, int gelu, hipStream_t s) {
     StashArgs part = a;
     part.unit0 = u;
     const dim3 grid((unsigned)((std::min(units - u, most) + 3) / 4));
-    if (!gelu) hipLaunchKernelGGL((stash_pack_kernel<0, 0>), grid, dim3(256), 0, s, part);
-    else if ((int64_t)a.p * a.M * a.F * 2 >= kStreamBytes) hipLaunchKernelGGL((stash_pack_kernel<1, 1>), grid, dim3(256), 0, s, part);
+    const int64_t bytes = (int64_t)a.p * a.M * a.F * 2;
+    if (!gelu && bytes >= kStreamBytes / 2) hipLaunchKernelGGL((stash_pack_kernel<0, 1>), grid, dim3(256), 0, s, part);
+    else if (!gelu) hipLaunchKernelGGL((stash_pack_kernel<0, 0>), grid, dim3(256), 0, s, part);
+    else if (bytes >= kStreamBytes) hipLaunchKernelGGL((stash_pack_kernel<1, 1>), grid, dim3(256), 0, s, part);
     else hipLaunchKernelGGL((stash_pack_kernel<1, 0>), grid, dim3(256), 0, s, part);
   }
   return hipGetLastError();
