@@ -19,7 +19,7 @@ constexpr int kStashBlock = 32;      // 8-bit activations: one scale per 32 x 32
 // Outputs of this many bytes and more, the memory-side cache's size, are stored
 // past the caches: no reader finds them there, and on their way through they
 // cost lines still to be read (norm backward of 8192 x 8192 160 -> 155 us, GeLU
-// backward of 8 x 2048 x 6144 128 -> 122).  Smaller ones stay for the kernel that
+// backward of 8 x 2048 x 6144 128 -> 122 us).  Smaller ones stay for the kernel that
 // reads them next: past the caches a norm of 4096 x 4096 takes 24.5 us by itself
 // instead of 28.1, but norm, matrix product and norm of 2048 x 8192 216 instead of
 // 204 and of 4096 x 8192 270 instead of 259.
@@ -51,7 +51,8 @@ struct NormArgs {
   uint32_t row0;                     // forward: the launch's first row
 };
 
-// Workgroups of the backward's row pass: a pure function of M and H.
+// Workgroups of the backward's row pass: a pure function of M and H, so that the
+// workspace can be asked for without a GPU and the sums' order is the same on all.
 int norm_backward_groups(int64_t M, int64_t H);
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_block_norm_backward(const NormArgs& a, hipStream_t s);

@@ -11,9 +11,10 @@
 // the two means.  Sums, statistics and weight gradients are fp32.
 //
 // Bound by memory, at the rate of a large copy (4.75 TB/s) or above: forward of
-// 4096 x 4096 bf16 28 us (4.8 TB/s), of 2048 x 12288 fp32 from four partials 125 us
-// (5.2 TB/s).  A decode step's 16 x 8192 takes 5.2 us, of which a launch alone is
-// 2.3: the rest is one row's chain of load, sum, exchange, sum, store.
+// 4096 x 4096 bf16 28 us a call (4.7 TB/s), of 2048 x 12288 fp32 from four partials
+// 126 (5.2 TB/s), of 2048 x 32768 bf16 134 (4.0 TB/s).  A decode step's 16 x 8192
+// takes 5.6 us of the GPU, of which a launch alone is 2.3: the rest is one row's
+// chain of load, sum, exchange, sum, store.
 #include <algorithm>
 
 #include "tpf_block.hpp"
@@ -230,14 +231,19 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs args) {
 // gate gradient is Q (w_post + o), so two sums serve three gradients.
 // Workgroup i adds rows i, i + groups, ... in registers; norm_columns_kernel
 // adds the workgroups in a fixed order.
-// Bound by memory for long columns (8192 x 8192 bf16: 148 us and 7 for the column
-// sums, 5.2 TB/s); 1003 x 5000 fp32 takes 25 and 4 us (3.1 TB/s), four rows a
-// workgroup one after the other and the start of both launches.
+// Bound by memory for long columns (8192 x 8192 bf16: 147 us and 7 for the column
+// sums, 5.2 TB/s).  1003 x 5000 with fp32 rows and vectors takes 27 and 4 us
+// (3.1 TB/s): four rows a workgroup one after the other, each with its vectors read
+// again in both halves, and the start of both launches.
 // With V = 1 (rows of up to 8192) a thread loads the next row before it joins
 // the current one, so that the row's barrier does not leave the memory idle,
-// and keeps its columns' bf16 weights and gate.  16 waves leave 128 registers a
-// thread: longer rows are read again from the cache after the sums instead of
-// being held, and so are fp32 weights.
+// and keeps its columns' bf16 weights and gate.  The bound of 16 waves leaves 128
+// registers a thread, in shorter rows too: rows past 8192 are read again from the
+// cache after the sums instead of being held, and so are fp32 weights.  That does
+// not keep every instance within the registers: the ones with bf16 rows and V = 1
+// spill two at most, those with fp32 rows or V = 2 up to 25, those with V = 4 from
+// 105 to 148 (200 to 268 bytes a lane), which bounds them: 2048 x 32768 takes
+// 474 us in bf16 (1.7 TB/s) and 636 in fp32, 2048 x 12288 in fp32 162 (3.1 TB/s).
 template <int XF, int BF, int WF, int V, int STREAM>
 __global__ __launch_bounds__(1024) void block_norm_backward_kernel(NormArgs args) {
   (void)args;

@@ -269,8 +269,9 @@ __device__ __forceinline__ void qw_store(const QweightArgs& a, int m, int n, flo
 // Bound by the cache accesses, not by the bytes or the arithmetic: a read of
 // the codes alone in this pattern takes 6.6 us for 8192 x 8192, the same kernel
 // without X's loads 3 us less, without the unpacking the same.  One row, groups
-// of 128: 12.4 us (2.7 TB/s); 16 rows over 8 shards of 1024, groups of 32 with
-// zero points: 16.6 us (23.3 with a scale and zero point loaded per lane).
+// of 128: 11.9 us a call (2.9 TB/s); 16 rows over 8 shards of 1024, groups of 32
+// with zero points: 17.9 us (6.5 more with a scale and zero point loaded per lane),
+// in a call of 21.5.
 // ---------------------------------------------------------------------------
 template <int NB, int W, int D, int RUNS>
 __global__ __launch_bounds__(64 * W) void qweight_few_kernel(QweightArgs args) {
@@ -374,9 +375,9 @@ __global__ __launch_bounds__(64 * W) void qweight_few_kernel(QweightArgs args) {
 // the four waves that need it; its 16-byte chunks are swizzled by the row, so
 // that the 16 rows of an operand read hit every bank.
 //
-// 64 rows, 8 shards of 3584 x 8192, groups of 64: 64 us and 7 for the sum of
-// the four parts, where one 32-column block a wave with X from the cache took
-// 141; bound by the waits between a unit's operand reads, products and sums at
+// 64 rows, 8 shards of 3584 x 8192, groups of 64: 67 us a call, 5 of them for the
+// sum of the four parts, where one 32-column block a wave with X from the cache
+// took 141; bound by the waits between a unit's operand reads, products and sums at
 // two waves a SIMD (four waves' registers do not hold 64 rows: 266 us).
 // ---------------------------------------------------------------------------
 template <int MB, int RUNS>

@@ -91,8 +91,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // read u itself: smaller than half the memory-side cache it is loaded through
 // the caches (pack of 4096 x 4096 and four products of it 365 us, past them 370),
 // larger it is not (8192 x 8192: 944 us either way, the pack alone 39 against 37).
-// Bound by memory: 4 x 4096 x 4096 with GeLU in 64 us, 5.25 TB/s, a large copy's
-// rate and more (73 us with u and the codes through the caches).
+// Bound by memory: 4 x 4096 x 4096 with GeLU in 63 us a call, 5.3 TB/s, a large
+// copy's rate and more (10 us longer with u and the codes through the caches).
 template <int GELU, int STREAM>
 __global__ __launch_bounds__(256) void stash_pack_kernel(StashArgs args) {
   (void)args;
@@ -175,7 +175,7 @@ hipError_t launch_stash_pack(const StashArgs& a, int gelu, hipStream_t s) {
 }
 
 // du = dh (Phi(u) + u phi(u)) and h = u Phi(u) from the stored values, eight
-// columns a lane.  Bound by memory: 8 x 2048 x 6144 in 121 us, 5.8 TB/s.
+// columns a lane.  Bound by memory: 8 x 2048 x 6144 in 122 to 124 us a call, 5.7 TB/s.
 template <int STREAM>
 __global__ __launch_bounds__(256) void stash_backward_kernel(StashArgs args) {
   (void)args;

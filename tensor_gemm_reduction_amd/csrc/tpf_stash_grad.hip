@@ -11,9 +11,11 @@
 // step t + 2 go out between the MFMAs of step t's first three slices, one or
 // two at a time, into the slot that step t - 1 left.
 //
-// 4 shards of 4096^3: 435 us, 1263 TFLOP/s, what a large library product of bf16
-// reaches on the card (1264): bound by the matrix cores at the clock they are held
-// to.  2 x [1003, 1352 x 2056]: 19.7 us (566 TFLOP/s): 374 tiles of 128 x 128 leave
+// 4 shards of 4096^3: 441 us a call, 1246 TFLOP/s, where a large library product of
+// bf16 reaches 1259 on the same card: bound by the matrix cores at the clock they
+// are held to (under a profiler 462 us there, 481 on a card whose library product
+// reaches 1202).
+// 2 x [1003, 1352 x 2056]: 19.0 us a call (586 TFLOP/s): 374 tiles of 128 x 128 leave
 // 138 of 256 compute units with one tile and 118 with two, 0.8 us a step of 64 rows,
 // and about 8 us go to the start, the first loads and the stores (10 with two-byte
 // stores).
