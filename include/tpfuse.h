@@ -364,7 +364,7 @@ int tpf_block_norm_backward(tpf_handle h, int p, int64_t M, int64_t H, const voi
  * the block's largest finite magnitude within 448 of it.  codes[k] [M, F] are
  * OCP e4m3 values of u 2^(127-e), rounded to nearest even, and NaN where u is
  * not finite.  With gelu != 0 the same pass writes act[k] [M, F] bf16 =
- * GeLU(u) (erf form, in fp32 to 2^-16 of the value, rounded once); otherwise
+ * GeLU(u) (erf form, in fp32 to 2^-15 of the value, rounded once); otherwise
  * act is ignored.
  * F must be a multiple of 8; codes are 8-byte aligned, scales any byte. */
 int tpf_stash_pack(tpf_handle h, int p, int64_t M, int64_t F, const void* const* u, int gelu, void* const* act,
