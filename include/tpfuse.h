@@ -408,6 +408,126 @@ int tpf_qweight_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, int
 /* Bytes of workspace of tpf_qweight_matmul (0: none needed, or invalid sizes). */
 size_t tpf_qweight_matmul_ws(int p, int64_t M, int64_t K, int64_t N, int group);
 
+/* ---------------------------------------------------------------------------
+ * Linears in 8 bits.  Operands are OCP e4m3 codes with a scale for each block of
+ * 128 along the contraction; sums are fp32.  Conventions as above.
+ *
+ * A packed operand [M, K] is codes [M, K] and scales [M, S], S = ceil(K / 128)
+ * rounded up to a multiple of 4: byte e of block b stands for 2^(e-127), so row m
+ * holds code[m][j] 2^(scales[m][j / 128] - 127).  K is a multiple of 16.
+ * ------------------------------------------------------------------------- */
+
+/* Scales of a weight's blocks of 128 x 128. */
+#define TPF_SCALE_BYTE 0         /* bytes, 2^(e-127) */
+#define TPF_SCALE_F32 1          /* fp32 factors */
+
+/* Packs u[k] [M, K] bf16: scales hold the least power of two, not below 2^-117,
+ * that keeps each block's largest finite magnitude within 448 of it (the bytes
+ * of blocks past K are 10, as a block of zeros has), codes the values of
+ * u 2^(127-e) rounded to nearest even, NaN where u is not finite.
+ *   codes, scales: the rows packed, or both NULL.
+ *   codes_t, scales_t: the transpose packed, [K, Mt] and [K, S of Mt], or both
+ *   NULL: u's rows down columns, as the weight gradients take them.  Mt is M
+ *   rounded up to a multiple of 128.  With E > 0 the columns are R rows of
+ *   experts (offsets, src as tpf_expert_route gives them), each expert's from a
+ *   block of 128 of its own on, in Mt = tpf_expert_columns(R, E) columns: row r
+ *   is u's row r (top = 0, R = M), or row src[r] / top (R = M top).  Columns of
+ *   no row are zeros. */
+int tpf_scaled_pack(tpf_handle h, int p, int64_t M, int64_t K, const void* const* u, void* const* codes,
+                    void* const* scales, void* const* codes_t, void* const* scales_t, int64_t E,
+                    const int32_t* offsets, const int32_t* src, int top, void* stream);
+
+/* Columns of the packed transpose of R rows of E experts (0 for invalid sizes). */
+int64_t tpf_expert_columns(int64_t R, int64_t E);
+
+/* Y = sum_k X[k] W_k^T, row-parallel over the shards (p = 1: any Linear).
+ *   X[k], x_scales[k]: [M, K] packed.
+ *   W[k]: [N, K] codes; w_scales[k]: [ceil(N/128), ceil(K/128)] of w_scale_type.
+ *   Y: [M, N] of y_dtype; with gelu != 0 GeLU of the fp32 sum.
+ * N must be a multiple of 8, x_scales 4-byte aligned, w_scales as their type. */
+int tpf_scaled_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, const void* const* X,
+                      const void* const* x_scales, const void* const* W, const void* const* w_scales,
+                      int w_scale_type, int gelu, void* Y, int y_dtype, void* stream);
+
+/* Weight gradients dW[k] = A_k B_k^T of shards k, from operands packed down
+ * columns (tpf_scaled_pack's transposes): A[k] [R, Mt], B[k] [C, Mt], dW[k]
+ * [R, C] of dw_dtype; the sum runs over the Mt columns, a multiple of 128.
+ * C must be a multiple of 8. */
+int tpf_scaled_weight_grad(tpf_handle h, int p, int64_t Mt, int64_t R, int64_t C, const void* const* A,
+                           const void* const* a_scales, const void* const* B, const void* const* b_scales,
+                           void* const* dW, int dw_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The MLP block of experts.  A token's k experts are its slots, numbered t k + j;
+ * each slot of a routed token has a row, and rows are sorted by expert, within an
+ * expert by slot.
+ * ------------------------------------------------------------------------- */
+
+#define TPF_SCORE_SOFTMAX 0
+#define TPF_SCORE_SIGMOID 1
+#define TPF_EXPERT_MAX_E 1024
+#define TPF_EXPERT_MAX_K 16
+#define TPF_EXPERT_MAX_GROUPS 16
+
+/* Routes T tokens to k of E experts each.
+ *   logits: [T, E] of dtype; bias: [E] fp32 or NULL; mask: [T] bytes or NULL,
+ *   0 for tokens that are not routed (padding).
+ * s = softmax(logits) over the E experts, or their sigmoid.  Experts are ordered
+ * by s + bias, compared as in 64 bits (without bias by the logit), the lowest
+ * number first among equals; NaN counts as the least.  With groups > 1 only
+ * experts of the top_groups groups of E / groups consecutive ones with the
+ * largest sums of their two largest s + bias can be chosen.
+ *   ids: [T, k], -1 for tokens that are not routed.
+ *   weights: [T, k] fp32: scale * s of the chosen, with renorm != 0 divided by
+ *   their sum (0 where that is 0); 0 for tokens that are not routed.
+ *   offsets: [E + 1], expert e's rows are offsets[e] .. offsets[e+1] - 1.
+ *   src: [T k], the slot of each row, -1 behind the last row.
+ *   pos: [T, k], the row of each slot, -1 for tokens that are not routed.
+ * All results are int32 but for weights.  k <= E / groups * top_groups. */
+int tpf_expert_route(tpf_handle h, int64_t T, int64_t E, int k, const void* logits, int dtype, int score,
+                     const float* bias, int groups, int top_groups, int renorm, double scale, const uint8_t* mask,
+                     int32_t* ids, float* weights, int32_t* offsets, int32_t* src, int32_t* pos, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* Bytes of workspace of tpf_expert_route (0 for invalid sizes). */
+size_t tpf_expert_route_ws(int64_t T, int64_t E);
+
+/* Gradient of the logits ([T, E] of dtype) from that of the weights ([T, k]
+ * fp32), the choice held; ids and weights as tpf_expert_route left them. */
+int tpf_expert_route_backward(tpf_handle h, int64_t T, int64_t E, int k, const void* logits, int dtype, int score,
+                              int renorm, double scale, const int32_t* ids, const float* weights,
+                              const float* dweights, void* dlogits, void* stream);
+
+/* The experts' products: row r of expert e becomes Y[r] = sum_k x W_k[e]^T.
+ *   X[k], x_scales[k]: packed rows, [R, K] (top = 0), or those of the tokens,
+ *   [R / top, K], of which row r takes row src[r] / top.
+ *   W[k]: [E, N, K] codes; w_scales[k]: [E, ceil(N/128), ceil(K/128)].
+ *   Y: [R, N] of y_dtype, R = T k; rows of no expert become zeros.
+ * As tpf_scaled_matmul otherwise.  Gathered rows must lie within 2 GiB. */
+int tpf_expert_matmul(tpf_handle h, int p, int64_t R, int64_t K, int64_t N, int64_t E, const void* const* X,
+                      const void* const* x_scales, const void* const* W, const void* const* w_scales,
+                      int w_scale_type, const int32_t* offsets, const int32_t* src, int top, int gelu, void* Y,
+                      int y_dtype, void* stream);
+
+/* The experts' weight gradients: dW[k] [E, R, C], dW[k][e] summed over expert
+ * e's rows.  A, B: packed by tpf_scaled_pack with the same offsets, Mt columns. */
+int tpf_expert_weight_grad(tpf_handle h, int p, int64_t Mt, int64_t R, int64_t C, int64_t E, const void* const* A,
+                           const void* const* a_scales, const void* const* B, const void* const* b_scales,
+                           const int32_t* offsets, void* const* dW, int dw_dtype, void* stream);
+
+/* y[t] = sum_j weights[t][j] rows[pos[t][j]] over the token's slots in order;
+ * rows [T k, H] of rows_dtype, y [T, H] of y_dtype, sums fp32; zeros for tokens
+ * that are not routed.  H must be a multiple of 8. */
+int tpf_expert_combine(tpf_handle h, int64_t T, int k, int64_t H, const void* rows, int rows_dtype,
+                       const float* weights, const int32_t* pos, void* y, int y_dtype, void* stream);
+
+/* Its gradients: drows[pos[t][j]] = weights[t][j] dy[t] (of rows_dtype; zeros in
+ * rows of no expert), dweights[t][j] = dy[t] . rows[pos[t][j]] (fp32; 0 for
+ * tokens that are not routed); dy [T, H] of dy_dtype. */
+int tpf_expert_combine_backward(tpf_handle h, int64_t T, int k, int64_t H, int64_t E, const void* dy, int dy_dtype,
+                                const void* rows, int rows_dtype, const float* weights, const int32_t* pos,
+                                const int32_t* offsets, void* drows, float* dweights, void* stream);
+
 /* Wait for the handle's work on `stream` to finish and report whether a
  * bounded wait inside the persistent kernel gave up since the last query
  * (TPF_ERR_TIMEOUT; the outputs of that call are then undefined).  Clears

@@ -114,6 +114,58 @@ inline int ktime_stop(tpf_handle h, hipStream_t s) {
   return TPF_OK;
 }
 
+// Nothing may unwind through the C ABI (building a message can run out of memory).
+template <class F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return TPF_ERR_INVALID_ARG;
+  }
+}
+
+// A size query: leaves the last error alone.
+template <class F>
+size_t guarded_size(F f) {
+  try {
+    const std::string saved = g_last_error;
+    const size_t n = f();
+    g_last_error = saved;
+    return n;
+  } catch (...) {
+    return 0;
+  }
+}
+
+inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+inline int check_ptrs_at(const void* const* arr, int count, const char* name, uintptr_t n) {
+  if (!arr) return fail(TPF_ERR_INVALID_ARG, std::string(name) + " array is NULL");
+  for (int i = 0; i < count; ++i) {
+    if (!arr[i]) return fail(TPF_ERR_INVALID_ARG, std::string(name) + "[" + std::to_string(i) + "] is NULL");
+    if (!aligned(arr[i], n))
+      return fail(TPF_ERR_ALIGNMENT,
+                  std::string(name) + "[" + std::to_string(i) + "] is not " + std::to_string(n) + "-byte aligned");
+  }
+  return TPF_OK;
+}
+
+inline int check_outs(void* const* arr, int count, const char* name, uintptr_t n) {
+  return check_ptrs_at(const_cast<const void* const*>(arr), count, name, n);
+}
+
+inline int check_shards(int p) {
+  if (p < 1 || p > kMaxShards) return fail(TPF_ERR_SHAPE, "p must be in [1, " + std::to_string(kMaxShards) + "]");
+  return TPF_OK;
+}
+
+inline int check_sizes(int64_t a, int64_t b, int64_t c, const char* names) {
+  if (a <= 0 || b <= 0 || c <= 0) return fail(TPF_ERR_SHAPE, std::string(names) + " must be positive");
+  if (a > INT32_MAX || b > INT32_MAX || c > INT32_MAX)
+    return fail(TPF_ERR_SHAPE, std::string(names) + " must fit in 31 bits");
+  return TPF_OK;
+}
+
 #define TPF_TIMED(h, s, launch)      \
   do {                               \
     int st_ = ktime_start((h), (s)); \

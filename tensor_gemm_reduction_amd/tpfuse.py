@@ -12,7 +12,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
-from typing import List, Optional, Sequence
+from typing import List, NamedTuple, Optional, Sequence
 
 import torch
 
@@ -30,6 +30,9 @@ ALLREDUCE, REDUCESCATTER = 0, 1
 OP_MATMUL_ALLREDUCE, OP_MATMUL_REDUCESCATTER, OP_ALLGATHER_MATMUL, OP_MATMUL_DX, OP_MLP_SP = range(5)
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 NORM_MAX_H = 32768
+SCALE_BYTE, SCALE_F32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+EXPERT_MAX_E, EXPERT_MAX_K, EXPERT_MAX_GROUPS = 1024, 16, 16
 MAX_SHARDS = 16
 MAX_CHUNKS = 64
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -68,6 +71,19 @@ SIGNATURES = {
     "tpf_stash_weight_grad": (_I, [_VP, _I, _I64, _I64, _I64, _PP, _PP, _PP, _PP, _I, _VP, _SZ, _VP]),
     "tpf_qweight_matmul_ws": (_SZ, [_I, _I64, _I64, _I64, _I]),
     "tpf_qweight_matmul": (_I, [_VP, _I, _I64, _I64, _I64, _I, _PP, _PP, _PP, _PP, _I, _VP, _I, _VP, _SZ, _VP]),
+    "tpf_scaled_pack": (_I, [_VP, _I, _I64, _I64, _PP, _PP, _PP, _PP, _PP, _I64, _VP, _VP, _I, _VP]),
+    "tpf_scaled_matmul": (_I, [_VP, _I, _I64, _I64, _I64, _PP, _PP, _PP, _PP, _I, _I, _VP, _I, _VP]),
+    "tpf_scaled_weight_grad": (_I, [_VP, _I, _I64, _I64, _I64, _PP, _PP, _PP, _PP, _PP, _I, _VP]),
+    "tpf_expert_columns": (_I64, [_I64, _I64]),
+    "tpf_expert_route_ws": (_SZ, [_I64, _I64]),
+    "tpf_expert_route": (_I, [_VP, _I64, _I64, _I, _VP, _I, _I, _VP, _I, _I, _I, ctypes.c_double, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                              _SZ, _VP]),
+    "tpf_expert_route_backward": (_I, [_VP, _I64, _I64, _I, _VP, _I, _I, _I, ctypes.c_double, _VP, _VP, _VP, _VP, _VP]),
+    "tpf_expert_matmul": (_I, [_VP, _I, _I64, _I64, _I64, _I64, _PP, _PP, _PP, _PP, _I, _VP, _VP, _I, _I, _VP, _I,
+                               _VP]),
+    "tpf_expert_weight_grad": (_I, [_VP, _I, _I64, _I64, _I64, _I64, _PP, _PP, _PP, _PP, _VP, _PP, _I, _VP]),
+    "tpf_expert_combine": (_I, [_VP, _I64, _I, _I64, _VP, _I, _VP, _VP, _VP, _I, _VP]),
+    "tpf_expert_combine_backward": (_I, [_VP, _I64, _I, _I64, _I64, _VP, _I, _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP]),
     "tpf_sync_status": (_I, [_VP, _VP]),
     "tpf_debug_set_wait": (_I, [_VP, _I64, _I]),
     "tpf_debug_set_delay": (_I, [_VP, ctypes.c_uint32, _I, _I]),
@@ -847,3 +863,333 @@ def qweight_matmul(X: Sequence[torch.Tensor], codes: Sequence[torch.Tensor], sca
                                     _dtype_code(Y.dtype), ws.data_ptr() if ws is not None else None,
                                     ws.numel() * ws.element_size() if ws is not None else 0, sp))
     return Y
+
+
+# ---------------------------------------------------------------------------
+# Linears in 8 bits, and the MLP block of experts.
+# ---------------------------------------------------------------------------
+
+SCALE_BLOCK = 128
+SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+_F8 = torch.float8_e4m3fn
+
+
+def fp8_scale_width(n: int) -> int:
+    """Scale bytes of a packed row of n values: one for each block of 128, rounded up to four."""
+    return -(-n // (4 * SCALE_BLOCK)) * 4
+
+
+def fp8_columns(rows: int, experts: Optional[int] = None) -> int:
+    """Columns of the packed transpose of `rows` rows: whole blocks of 128 (of so
+    many experts' rows: the most that any loads of the experts can need)."""
+    if experts is None:
+        return -(-rows // SCALE_BLOCK) * SCALE_BLOCK
+    return int(load().tpf_expert_columns(rows, experts))
+
+
+class ExpertRoute(NamedTuple):
+    """Where the tokens of a batch go (`expert_route`).  Slot t k + j is token t's
+    j-th expert; rows are sorted by expert, within an expert by slot."""
+    ids: torch.Tensor        # [T, k] int32: the experts of each token, -1: not routed
+    weights: torch.Tensor    # [T, k] fp32
+    offsets: torch.Tensor    # [E + 1] int32: expert e's rows are offsets[e] .. offsets[e + 1] - 1
+    src: torch.Tensor        # [T k] int32: the slot of each row, -1 behind the last row
+    pos: torch.Tensor        # [T, k] int32: the row of each slot, -1: none
+
+
+def _check_route(route, dev):
+    """(T, k, E, addresses of ids, weights, offsets, src, pos)."""
+    _need(isinstance(route, ExpertRoute), "route is not an ExpertRoute")
+    T, k = _matrix("route.ids", route.ids, "[T, k]")
+    _need(isinstance(route.offsets, torch.Tensor) and route.offsets.dim() == 1, "route.offsets is not a vector [E + 1]")
+    E = route.offsets.shape[0] - 1
+    at = _operands(dev.index, (route.ids, route.pos), torch.int32, (T, k), (route.weights,), torch.float32, (T, k),
+                   (route.offsets,), torch.int32, (E + 1,), (route.src,), torch.int32, (T * k,))
+    if at is None:
+        for name, shape, dtype in (("ids", (T, k), torch.int32), ("weights", (T, k), torch.float32),
+                                   ("offsets", (E + 1,), torch.int32), ("src", (T * k,), torch.int32),
+                                   ("pos", (T, k), torch.int32)):
+            _check("route." + name, [getattr(route, name)], shape, (dtype,), dev)
+    return T, k, E
+
+
+def fp8_pack(u: Sequence[torch.Tensor], rows: bool = True, columns: bool = False,
+             route: Optional[ExpertRoute] = None, gather: bool = False, handle: Optional[Handle] = None, stream=None):
+    """(codes, scales, codes_t, scales_t): u[k] ([M, K] bf16) in 8 bits, by rows for
+    the products (`rows`; None without) and by columns for the weight gradients
+    (`columns`; None without).
+
+    Codes are e4m3 and each block of 128 along a row shares one power of two, so
+    that u ~ codes * 2^(scales - 127); scales are [M, fp8_scale_width(K)] uint8.
+    By columns the same holds of the transpose, [K, Mt] with Mt =
+    `fp8_columns(M)`, rows behind the last being zeros.  With `route` the columns
+    are the experts' rows, each expert's in blocks of its own: of u as it lies (M =
+    T k), or with `gather` of the tokens that u holds (M = T).  K is a multiple of
+    16."""
+    p = len(u)
+    _need(p >= 1, "u: no shards given")
+    M, K = _matrix("u[0]", u[0], "[M, K]")
+    _need(rows or columns, "fp8_pack: neither rows nor columns are asked for")
+    _need(route is not None or not gather, "gather needs a route")
+    dev = u[0].device
+    at = _operands(u[0].get_device(), u, torch.bfloat16, (M, K))
+    if at is None:
+        _check("u", u, (M, K))
+        at = (_ptrs(u),)
+    T, k, E = (0, 0, 0) if route is None else _check_route(route, dev)
+    if route is not None:
+        _need(M == (T if gather else T * k), f"u has {M} rows, expected {T if gather else T * k} of the route")
+    codes = scales = codes_t = scales_t = cat = sat = ctat = stat = None
+    with _on(stream):
+        if rows:
+            codes, cat, scales, sat = _shards(dev, p, _F8, (M, K), torch.uint8, (M, fp8_scale_width(K)))
+        if columns:
+            Mt = fp8_columns(M) if route is None else fp8_columns(T * k, E)
+            _need(Mt > 0, f"route has {E} experts, expected 1 to {EXPERT_MAX_E}")
+            codes_t, ctat, scales_t, stat = _shards(dev, p, _F8, (K, Mt), torch.uint8, (K, fp8_scale_width(Mt)))
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_scaled_pack(h, p, M, K, at[0], cat, sat, ctat, stat, E,
+                                 route.offsets.data_ptr() if E else None,
+                                 route.src.data_ptr() if gather else None, k if gather else 0, sp))
+    return codes, scales, codes_t, scales_t
+
+
+def _packed(name: str, codes, scales, shape, dev):
+    """Addresses of packed operands and their scales."""
+    scale_shape = shape[:-1] + (fp8_scale_width(shape[-1]),)
+    at = _operands(dev.index, codes, _F8, shape, scales, torch.uint8, scale_shape)
+    if at is None:
+        _check(name, codes, shape, (_F8,), dev)
+        _check(name + "_scales", scales, scale_shape, (torch.uint8,), dev)
+        at = _ptrs(codes), _ptrs(scales)
+    return at
+
+
+def _scaled_weights(codes, scales, shape, dev):
+    """Addresses of weights with a scale for each 128 x 128 block, and the scales' type."""
+    blocks = shape[:-2] + (-(-shape[-2] // SCALE_BLOCK), -(-shape[-1] // SCALE_BLOCK))
+    dtype = getattr(scales[0], "dtype", None)
+    at = None
+    if dtype in (torch.uint8, torch.float32):
+        at = _operands(dev.index, codes, _F8, shape, scales, dtype, blocks)
+    if at is None:
+        _check("W", codes, shape, (_F8,), dev)
+        _check("w_scales", scales, blocks, (torch.uint8, torch.float32), dev)
+        _need(all(t.dtype == dtype for t in scales), "w_scales: the shards differ in dtype")
+        at = _ptrs(codes), _ptrs(scales)
+    return at, SCALE_F32 if dtype == torch.float32 else SCALE_BYTE
+
+
+def _result(name: str, Y, dtype, shape, dev, stream):
+    """The caller's output, or a new one."""
+    if Y is None:
+        _need(dtype in OUT_DTYPES, f"output dtype must be bfloat16 or float32, got {dtype}")
+        with _on(stream):
+            Y, = _empty(dev, dtype, shape)
+    else:
+        _check(name, [Y], shape, OUT_DTYPES, dev)
+    return Y
+
+
+def fp8_matmul(X: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor], W: Sequence[torch.Tensor],
+               w_scales: Sequence[torch.Tensor], gelu: bool = False, out_dtype=torch.bfloat16,
+               Y: Optional[torch.Tensor] = None, handle: Optional[Handle] = None, stream=None) -> torch.Tensor:
+    """Y = sum_k X[k] W_k^T in 8 bits (row-parallel over the shards; p = 1: any
+    Linear), GeLU of it with `gelu`.
+
+    X[k], x_scales[k]: [M, K] as `fp8_pack` leaves it; W[k] [N, K] e4m3 with a scale
+    for each 128 x 128 block, w_scales[k] [ceil(N/128), ceil(K/128)]: fp32 factors,
+    or uint8 powers of two 2^(w_scales - 127).  An input gradient is the same
+    product with the transposed weight."""
+    p = len(X)
+    _need(p >= 1, "X: no shards given")
+    M, K = _matrix("X[0]", X[0], "[M, K]")
+    _check_shards("x_scales", x_scales, p)
+    _check_shards("W", W, p)
+    _check_shards("w_scales", w_scales, p)
+    N, _ = _matrix("W[0]", W[0], "[N, K]")
+    dev = X[0].device
+    _need(dev.type == "cuda", f"X[0] is on {dev}, not on a GPU")
+    xat = _packed("X", X, x_scales, (M, K), dev)
+    wat, kind = _scaled_weights(W, w_scales, (N, K), dev)
+    Y = _result("Y", Y, out_dtype, (M, N), dev, stream)
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_scaled_matmul(h, p, M, K, N, *xat, *wat, kind, 1 if gelu else 0, Y.data_ptr(),
+                                   _dtype_code(Y.dtype), sp))
+    return Y
+
+
+def _weight_grad_operands(A, a_scales, B, b_scales):
+    p = len(A)
+    _need(p >= 1, "A: no shards given")
+    R, Mt = _matrix("A[0]", A[0], "[R, Mt]")
+    _check_shards("a_scales", a_scales, p)
+    _check_shards("B", B, p)
+    _check_shards("b_scales", b_scales, p)
+    C, _ = _matrix("B[0]", B[0], "[C, Mt]")
+    dev = A[0].device
+    _need(dev.type == "cuda", f"A[0] is on {dev}, not on a GPU")
+    return dev, p, Mt, R, C, _packed("A", A, a_scales, (R, Mt), dev), _packed("B", B, b_scales, (C, Mt), dev)
+
+
+def _results(name: str, dW, p: int, dtype, shape, dev, stream):
+    """The caller's outputs of p shards, or new ones, and their addresses."""
+    if dW is None:
+        _need(dtype in OUT_DTYPES, f"output dtype must be bfloat16 or float32, got {dtype}")
+        with _on(stream):
+            dW, at = _shards(dev, p, dtype, shape)
+        return list(dW), at
+    _check_shards(name, dW, p)
+    _check(name, dW, shape, OUT_DTYPES, dev)
+    _need(all(d.dtype == dW[0].dtype for d in dW), f"{name}: the shards differ in dtype")
+    return dW, _ptrs(dW)
+
+
+def fp8_weight_grad(A: Sequence[torch.Tensor], a_scales: Sequence[torch.Tensor], B: Sequence[torch.Tensor],
+                    b_scales: Sequence[torch.Tensor], out_dtype=torch.float32, dW=None,
+                    handle: Optional[Handle] = None, stream=None) -> List[torch.Tensor]:
+    """dW[k] = A_k B_k^T for every shard k: `weight_grad` of operands in 8 bits.
+
+    A[k], a_scales[k]: [R, Mt] and B[k], b_scales[k]: [C, Mt], the inputs and the
+    outputs' gradients as `fp8_pack` leaves them by columns.  Row-parallel: B of
+    one gradient, p times; column-parallel: A of one input, p times."""
+    dev, p, Mt, R, C, aat, bat = _weight_grad_operands(A, a_scales, B, b_scales)
+    dW, wat = _results("dW", dW, p, out_dtype, (R, C), dev, stream)
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_scaled_weight_grad(h, p, Mt, R, C, *aat, *bat, wat, _dtype_code(dW[0].dtype), sp))
+    return dW
+
+
+def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                 groups: int = 1, top_groups: int = 1, renorm: bool = True, scale: float = 1.0,
+                 mask: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 handle: Optional[Handle] = None, stream=None) -> ExpertRoute:
+    """Routes each of T tokens to k of E experts; logits [T, E] bf16 or fp32.
+
+    s = softmax or sigmoid of the logits.  The k experts with the largest s + bias
+    are taken (bias [E] fp32, for balance; compared as in 64 bits, the lowest number
+    first among equals), with `groups` > 1 from the `top_groups` groups of
+    consecutive experts with the largest sums of their two largest.  Weights are
+    scale * s, divided by the sum of the chosen with `renorm`.  Tokens whose `mask`
+    ([T] bool) is false are not routed."""
+    T, E = _matrix("logits", logits, "[T, E]")
+    _need(score in SCORES, f"score must be one of {sorted(SCORES)}, got {score!r}")
+    dev = _check("logits", [logits], (T, E), OUT_DTYPES)
+    if bias is not None:
+        _check("bias", [bias], (E,), (torch.float32,), dev)
+    if mask is not None:
+        _check("mask", [mask], (T,), (torch.bool,), dev)
+    _check_ws(ws, dev)
+    need = load().tpf_expert_route_ws(T, E)
+    with _on(stream):
+        ids, weights, offsets, src, pos, new_ws = _empty(
+            dev, torch.int32, (T, k), torch.float32, (T, k), torch.int32, (E + 1,), torch.int32, (T * k,), torch.int32,
+            (T, k), torch.uint8, (max(need, 16),) if ws is None else None)
+    ws = new_ws if ws is None else ws
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_expert_route(h, T, E, k, logits.data_ptr(), _dtype_code(logits.dtype), SCORES[score],
+                                  bias.data_ptr() if bias is not None else None, groups, top_groups,
+                                  1 if renorm else 0, scale, mask.data_ptr() if mask is not None else None,
+                                  ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), src.data_ptr(),
+                                  pos.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), sp))
+    return ExpertRoute(ids, weights, offsets, src, pos)
+
+
+def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, route: ExpertRoute, score: str = "softmax",
+                          renorm: bool = True, scale: float = 1.0, handle: Optional[Handle] = None,
+                          stream=None) -> torch.Tensor:
+    """The gradient of `expert_route`'s logits (of their dtype) from that of its
+    weights ([T, k] fp32); the other arguments as they were there."""
+    T, E = _matrix("logits", logits, "[T, E]")
+    _need(score in SCORES, f"score must be one of {sorted(SCORES)}, got {score!r}")
+    dev = _check("logits", [logits], (T, E), OUT_DTYPES)
+    rT, k, rE = _check_route(route, dev)
+    _need((rT, rE) == (T, E), f"route is of {rT} tokens and {rE} experts, logits of {T} and {E}")
+    _check("dweights", [dweights], (T, k), (torch.float32,), dev)
+    with _on(stream):
+        dlogits, = _empty(dev, logits.dtype, (T, E))
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_expert_route_backward(h, T, E, k, logits.data_ptr(), _dtype_code(logits.dtype), SCORES[score],
+                                           1 if renorm else 0, scale, route.ids.data_ptr(), route.weights.data_ptr(),
+                                           dweights.data_ptr(), dlogits.data_ptr(), sp))
+    return dlogits
+
+
+def expert_matmul(X: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor], W: Sequence[torch.Tensor],
+                  w_scales: Sequence[torch.Tensor], route: ExpertRoute, gather: bool = False, gelu: bool = False,
+                  out_dtype=torch.bfloat16, Y: Optional[torch.Tensor] = None, handle: Optional[Handle] = None,
+                  stream=None) -> torch.Tensor:
+    """The experts' products: row r of expert e becomes Y[r] = sum_k x W_k[e]^T (Y
+    [T k, N]; rows of no expert are zeros), GeLU of it with `gelu`.
+
+    X[k], x_scales[k]: rows as `fp8_pack` leaves them, [T k, K] in the route's
+    order, or with `gather` those of the tokens, [T, K]; W[k] [E, N, K], w_scales[k]
+    [E, ceil(N/128), ceil(K/128)] as `fp8_matmul` takes them."""
+    p = len(X)
+    _need(p >= 1, "X: no shards given")
+    M, K = _matrix("X[0]", X[0], "[T, K]" if gather else "[T k, K]")
+    _check_shards("x_scales", x_scales, p)
+    _check_shards("W", W, p)
+    _check_shards("w_scales", w_scales, p)
+    dev = X[0].device
+    _need(dev.type == "cuda", f"X[0] is on {dev}, not on a GPU")
+    T, k, E = _check_route(route, dev)
+    _need(M == (T if gather else T * k), f"X[0] has {M} rows, expected {T if gather else T * k} of the route")
+    _need(isinstance(W[0], torch.Tensor) and W[0].dim() == 3, "W[0] is no tensor [E, N, K]")
+    N = W[0].shape[1]
+    xat = _packed("X", X, x_scales, (M, K), dev)
+    wat, kind = _scaled_weights(W, w_scales, (E, N, K), dev)
+    Y = _result("Y", Y, out_dtype, (T * k, N), dev, stream)
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_expert_matmul(h, p, T * k, K, N, E, *xat, *wat, kind, route.offsets.data_ptr(),
+                                   route.src.data_ptr(), k if gather else 0, 1 if gelu else 0, Y.data_ptr(),
+                                   _dtype_code(Y.dtype), sp))
+    return Y
+
+
+def expert_weight_grad(A: Sequence[torch.Tensor], a_scales: Sequence[torch.Tensor], B: Sequence[torch.Tensor],
+                       b_scales: Sequence[torch.Tensor], route: ExpertRoute, out_dtype=torch.float32, dW=None,
+                       handle: Optional[Handle] = None, stream=None) -> List[torch.Tensor]:
+    """dW[k] [E, R, C]: `fp8_weight_grad` over each expert's rows by itself, of
+    operands that `fp8_pack` packed by columns with this route."""
+    dev, p, Mt, R, C, aat, bat = _weight_grad_operands(A, a_scales, B, b_scales)
+    T, k, E = _check_route(route, dev)
+    _need(Mt == fp8_columns(T * k, E), f"A[0] has {Mt} columns, expected {fp8_columns(T * k, E)} of the route")
+    dW, wat = _results("dW", dW, p, out_dtype, (E, R, C), dev, stream)
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_expert_weight_grad(h, p, Mt, R, C, E, *aat, *bat, route.offsets.data_ptr(), wat,
+                                        _dtype_code(dW[0].dtype), sp))
+    return dW
+
+
+def expert_combine(rows: torch.Tensor, route: ExpertRoute, out_dtype=torch.bfloat16,
+                   Y: Optional[torch.Tensor] = None, handle: Optional[Handle] = None, stream=None) -> torch.Tensor:
+    """Y[t] = sum_j route.weights[t, j] rows[route.pos[t, j]]: the sum of each
+    token's rows ([T k, H] bf16 or fp32); zeros for tokens that are not routed."""
+    R, H = _matrix("rows", rows, "[T k, H]")
+    dev = _check("rows", [rows], (R, H), OUT_DTYPES)
+    T, k, E = _check_route(route, dev)
+    _need(R == T * k, f"rows has {R} rows, expected {T * k} of the route")
+    Y = _result("Y", Y, out_dtype, (T, H), dev, stream)
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_expert_combine(h, T, k, H, rows.data_ptr(), _dtype_code(rows.dtype), route.weights.data_ptr(),
+                                    route.pos.data_ptr(), Y.data_ptr(), _dtype_code(Y.dtype), sp))
+    return Y
+
+
+def expert_combine_backward(dy: torch.Tensor, rows: torch.Tensor, route: ExpertRoute,
+                            handle: Optional[Handle] = None, stream=None):
+    """(drows, dweights) of `expert_combine` from dy ([T, H] bf16 or fp32): drows of
+    the rows' dtype, zeros in rows of no expert; dweights [T, k] fp32."""
+    R, H = _matrix("rows", rows, "[T k, H]")
+    dev = _check("rows", [rows], (R, H), OUT_DTYPES)
+    T, k, E = _check_route(route, dev)
+    _need(R == T * k, f"rows has {R} rows, expected {T * k} of the route")
+    _check("dy", [dy], (T, H), OUT_DTYPES, dev)
+    with _on(stream):
+        drows, dweights = _empty(dev, rows.dtype, (R, H), torch.float32, (T, k))
+    h, sp = _ctx(handle, dev, stream)
+    check(load().tpf_expert_combine_backward(h, T, k, H, E, dy.data_ptr(), _dtype_code(dy.dtype), rows.data_ptr(),
+                                             _dtype_code(rows.dtype), route.weights.data_ptr(), route.pos.data_ptr(),
+                                             route.offsets.data_ptr(), drows.data_ptr(), dweights.data_ptr(), sp))
+    return drows, dweights
