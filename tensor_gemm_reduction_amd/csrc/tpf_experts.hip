@@ -21,272 +21,699 @@ __device__ __forceinline__ float value_at(const void* p, int64_t i) {
   return F32 ? reinterpret_cast<const float*>(p)[i] : bf16_at(p, i);
 }
 
-constexpr int kRouteThreads = 1024;
+constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
 constexpr int kRouteTokens = 64;       // tokens of a part of the order, at least
 constexpr double kNone = -__builtin_huge_val();
 
-template <int L>
-__device__ __forceinline__ double max_over(double v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v = fmax(v, __shfl_xor(v, d));
+// Data-parallel moves within rows of 16 lanes: one vector instruction for each 32
+// bits, where an exchange through the LDS crossbar takes over 100 cycles.
+constexpr int kRowShr = 0x110, kRowRor = 0x120, kRowBcast = 0x150;
+template <int CTRL, class T>
+__device__ __forceinline__ T dpp(T v) {
+  if constexpr (sizeof(T) == 8) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
+  } else {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+  }
+}
+// f over the L lanes (16 or 64) that share a token, in all of them.
+template <int L, class T, class F>
+__device__ __forceinline__ T over(T v, F f) {
+  static_assert(L == 16 || L == 64, "rows of 16 lanes, or all");
+  v = f(v, dpp<kRowRor + 8>(v));
+  v = f(v, dpp<kRowRor + 4>(v));
+  v = f(v, dpp<kRowRor + 2>(v));
+  v = f(v, dpp<kRowRor + 1>(v));
+  if constexpr (L == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
   return v;
 }
+template <int L, class T>
+__device__ __forceinline__ T max_over(T v) {
+  return over<L>(v, [](T x, T y) { return max(x, y); });
+}
+template <int L, class T>
+__device__ __forceinline__ T min_over(T v) {
+  return over<L>(v, [](T x, T y) { return min(x, y); });
+}
+template <int L, class T>
+__device__ __forceinline__ T sum_over(T v) {
+  return over<L>(v, [](T x, T y) { return x + y; });
+}
+// The sum up to and with this lane.
 template <int L>
-__device__ __forceinline__ double sum_over(double v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d);
+__device__ __forceinline__ int sum_upto(int v, int li) {
+  v += dpp<kRowShr + 1>(v);
+  v += dpp<kRowShr + 2>(v);
+  v += dpp<kRowShr + 4>(v);
+  v += dpp<kRowShr + 8>(v);
+  if constexpr (L == 64) {
+    int o = __shfl(v, (li & 48) - 1);
+    if (li & 16) v += o;
+    o = __shfl(v, 31);
+    if (li & 32) v += o;
+  }
   return v;
+}
+// f(j, v of lane j) for the L lanes that share a token.
+template <int L, int J = 0, class T, class F>
+__device__ __forceinline__ void each_lane(T v, F f) {
+  if constexpr (J < L) {
+    if constexpr (L == 16) f(J, dpp<kRowBcast + J>(v));
+    else f(J, __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), J)));
+    each_lane<L, J + 1>(v, f);
+  }
 }
 // The largest value's index, the lowest among equals; index INT_MAX: nothing.
-template <int L>
 __device__ __forceinline__ int best_over(double v, int at) {
 #pragma unroll
-  for (int d = 1; d < L; d <<= 1) {
+  for (int d = 1; d < 64; d <<= 1) {
     const double ov = __shfl_xor(v, d);
     const int oa = __shfl_xor(at, d);
     if (ov > v || (ov == v && oa < at)) v = ov, at = oa;
   }
   return at;
 }
+// Lanes of one wave exchange values through LDS: its accesses stay in order.
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
-// The order of the experts' rows, part b of the tokens: each expert's rows
-// follow those of the experts before it and of its own in earlier parts, in the
-// order of the slots.  One thread an expert walks the part's slots, so the order
-// needs no atomics.
-constexpr int kOrderSlots = 4096;
-__device__ void order_part(const RouteArgs& a, int b, int* lds_total, uint16_t* lds_ids) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int lane = tid & 63;
-  // Rows of every expert, then the first row of each (one wave, 64 at a time).
-  for (int e = tid; e < a.E; e += nt) {
-    int total = 0;
-    for (int c = 0; c < a.chunks; ++c) total += a.hist[(int64_t)c * a.E + e];
-    lds_total[e] = total;
-  }
-  __syncthreads();
-  if (tid < 64) {
+// ---------------------------------------------------------------------------
+// The order of the experts' rows.
+//
+// Each part of the tokens has counted its rows of every expert (hist[e][part],
+// 16 bits).  An expert's rows of part b begin behind those of the experts before
+// it and its own of earlier parts; within a part, waves take 64 slots at a time:
+// ballots over the expert numbers' bits give each slot the number of equal ones
+// before it in its wave, a count a wave and expert the number in the waves
+// before.  No atomics, so the order is always that of the slots.
+// ---------------------------------------------------------------------------
+struct OrderLds {
+  int base[kExpertMaxE + 1];                     // rows of every expert; then its next row
+  int before[kExpertMaxE];                       // rows of every expert in earlier parts
+  uint16_t wave[kRouteWaves][kExpertMaxE];       // rows of the waves before
+};
+
+__device__ void order_part(const RouteArgs& a, int b, OrderLds& lds) {
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  if (tid < 64) {                                // totals -> first rows, 64 experts at a time
     int before = 0;
     for (int base = 0; base < a.E; base += 64) {
       const int e = base + lane;
-      const int n = e < a.E ? lds_total[e] : 0;
-      int upto = n;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(upto, d);
-        if (lane >= d) upto += v;
-      }
-      if (e < a.E) lds_total[e] = before + upto - n;
-      before += __shfl(upto, 63);
+      const int n = e < a.E ? lds.base[e] : 0;
+      const int upto = sum_upto<64>(n, lane);
+      if (e < a.E) lds.base[e] = before + upto - n;
+      before += __builtin_amdgcn_readlane(upto, 63);
     }
-    if (lane == 0) lds_total[a.E] = before;
+    if (lane == 0) lds.base[a.E] = before;
   }
   __syncthreads();
+  const int R = a.T * a.k, used = lds.base[a.E];
   if (b == 0)
-    for (int e = tid; e <= a.E; e += nt) a.offsets[e] = lds_total[e];
-  const int R = a.T * a.k;
-  // Rows behind the last expert's have no slot.
-  for (int64_t r = (int64_t)lds_total[a.E] + (int64_t)b * nt + tid; r < R; r += (int64_t)a.chunks * nt) a.src[r] = -1;
+    for (int e = tid; e <= a.E; e += kRouteThreads) a.offsets[e] = lds.base[e];
+  for (int64_t r = (int64_t)used + (int64_t)b * kRouteThreads + tid; r < R; r += (int64_t)a.chunks * kRouteThreads)
+    a.src[r] = -1;                               // rows behind the last expert's have no slot
+  if (a.chunks > 1) {
+    __syncthreads();
+    for (int e = tid; e < a.E; e += kRouteThreads) lds.base[e] += lds.before[e];
+  }
   const int64_t first = (int64_t)b * a.chunk * a.k;
   const int64_t last = min((int64_t)R, first + (int64_t)a.chunk * a.k);
-  for (int e0 = 0; e0 < a.E; e0 += nt) {
-    const int e = e0 + tid;
-    int row = 0;
-    if (e < a.E) {
-      row = lds_total[e];
-      for (int c = 0; c < b; ++c) row += a.hist[(int64_t)c * a.E + e];
+  int id_bits = 0;
+  while (1 << id_bits < a.E) ++id_bits;
+  for (int64_t s0 = first; s0 < last; s0 += kRouteThreads) {
+    __syncthreads();
+    for (int i = tid; i < kRouteWaves * kExpertMaxE / 8; i += kRouteThreads)
+      reinterpret_cast<u32x4_t*>(lds.wave)[i] = u32x4_t{0, 0, 0, 0};
+    __syncthreads();
+    const int64_t slot = s0 + tid;
+    const int id = slot < last ? a.ids[slot] : -1;
+    uint64_t peers = __ballot(id >= 0);
+    for (int i = 0; i < id_bits; ++i) {
+      const uint64_t set = __ballot(id >> i & 1);
+      peers &= id >> i & 1 ? set : ~set;
     }
-    for (int64_t s0 = first; s0 < last; s0 += kOrderSlots) {
-      const int n = (int)min((int64_t)kOrderSlots, last - s0);
-      __syncthreads();
-      for (int i = tid; i < n; i += nt) {
-        const int id = a.ids[s0 + i];
-        lds_ids[i] = (uint16_t)id;
-        if (id < 0) a.pos[s0 + i] = -1;
+    const int rank = __popcll(peers & ((1ull << lane) - 1));
+    if (id >= 0 && rank == 0) lds.wave[w][id] = (uint16_t)__popcll(peers);
+    __syncthreads();
+    int total = 0;
+    if (tid < a.E)
+#pragma unroll
+      for (int i = 0; i < kRouteWaves; ++i) {
+        const int n = lds.wave[i][tid];
+        lds.wave[i][tid] = (uint16_t)total;
+        total += n;
       }
-      __syncthreads();
-      if (e < a.E)
-        for (int i = 0; i < n; ++i)
-          if (lds_ids[i] == e) {
-            a.pos[s0 + i] = row;
-            a.src[row] = (int)(s0 + i);
-            ++row;
-          }
+    __syncthreads();
+    if (id >= 0) {
+      const int row = lds.base[id] + lds.wave[w][id] + rank;
+      a.pos[slot] = row;
+      a.src[row] = (int)slot;
+    } else if (slot < last) {
+      a.pos[slot] = -1;
     }
+    __syncthreads();
+    if (tid < a.E) lds.base[tid] += total;
   }
 }
 
 __global__ __launch_bounds__(kRouteThreads) void expert_order_kernel(RouteArgs args) {
   (void)args;
-  __shared__ int total[kExpertMaxE + 1];
-  __shared__ uint16_t ids[kOrderSlots];
-  order_part(kernarg<RouteArgs>(), blockIdx.x, total, ids);
+  const RouteArgs& a = kernarg<RouteArgs>();
+  __shared__ OrderLds lds;
+  const int lane = threadIdx.x & 63;
+  // One wave an expert, four parts' counts a lane, eight experts' loads at a time.
+  const int wave = threadIdx.x >> 6;
+  for (int e0 = wave; e0 < a.E; e0 += 8 * kRouteWaves) {
+    int all[8] = {}, before[8] = {};
+    for (int c = lane * 4; c < a.chunks; c += 256) {
+      u32x2_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = *reinterpret_cast<const u32x2_t*>(a.hist + (int64_t)min(e0 + j * kRouteWaves, a.E - 1) * a.pad + c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = i & 1 ? (int)(v[j][i >> 1] >> 16) : (int)(v[j][i >> 1] & 0xffffu);
+          all[j] += c + i < a.chunks ? n : 0;
+          before[j] += c + i < (int)blockIdx.x ? n : 0;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      all[j] = sum_over<64>(all[j]);
+      before[j] = sum_over<64>(before[j]);
+      if (lane == 0 && e0 + j * kRouteWaves < a.E) {
+        lds.base[e0 + j * kRouteWaves] = all[j];
+        lds.before[e0 + j * kRouteWaves] = before[j];
+      }
+    }
+  }
+  __syncthreads();
+  order_part(a, blockIdx.x, lds);
 }
 
-// Routes one part of the tokens.  L lanes share a token, lane l holding the
-// experts l, l + L, ...; choices are compared in 64 bits, so that the order of
-// nearly equal values is the definition's.  With one part the order of the
-// experts' rows follows in the same launch.
+// ---------------------------------------------------------------------------
+// Scores, choice and weights.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+
+// A token's experts and weights once the choice is made: lane j < k of the L that
+// share the token holds the j-th expert.  top and sum: the softmax's (64 bits).
+template <int L, int F32>
+__device__ __forceinline__ void put_choice(const RouteArgs& a, int t, int li, int id, bool routed, double top, double sum,
+                                           int* hist) {
+  const bool mine = routed && li < a.k && (uint32_t)id < (uint32_t)a.E;
+  double s = 0.0;
+  if (mine) {
+    const double l = value_at<F32>(a.logits, (int64_t)t * a.E + id);
+    s = a.score == SCORE_SIGMOID ? sigmoid64(l) : (top == kNone ? 0.0 : exp(l - top));
+  }
+  if (a.renorm) sum = sum_over<L>(s);
+  if (li < a.k) {
+    double w = 0.0;
+    if (mine) w = a.renorm ? (sum == 0.0 ? 0.0 : a.scale * (s / sum)) :
+                  a.scale * (a.score == SCORE_SIGMOID || sum == 0.0 ? s : s / sum);
+    a.ids[(int64_t)t * a.k + li] = mine ? id : -1;
+    a.weights[(int64_t)t * a.k + li] = (float)w;
+    if (mine) atomicAdd(&hist[id], 1);
+  }
+}
+
+template <int L, int F32>
+__device__ __forceinline__ double softmax_sum(const RouteArgs& a, int64_t row, int li, double top) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int e = li; e < a.E; e += L) sum += exp((double)value_at<F32>(a.logits, row + e) - top);
+  return sum_over<L>(sum);
+}
+
+// One token by a whole wave, everything in 64 bits: the definition as it stands.
+// values: LDS of E numbers.
+template <int F32>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane, int* hist, double* values) {
+  const int64_t row = (int64_t)t * a.E;
+  const bool softmax = a.score == SCORE_SOFTMAX, scores = a.bias || a.groups > 1;
+  double top = kNone, sum = 1.0;
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) top = max(top, (double)value_at<F32>(a.logits, row + e));
+  top = max_over<64>(top);
+  if (softmax && (scores || !a.renorm)) sum = top == kNone ? 0.0 : softmax_sum<64, F32>(a, row, lane, top);
+  wave_lds();
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) {
+    const double l = value_at<F32>(a.logits, row + e);
+    double v = l;
+    if (scores) v = softmax ? (top == kNone ? 0.0 : exp(l - top) / sum) : sigmoid64(l);
+    if (a.bias) v += (double)a.bias[e];
+    values[e] = v == v ? v : kNone;
+  }
+  wave_lds();
+  uint32_t allowed = ~0u;
+  const int gs = a.E / a.groups;
+  if (a.groups > 1) {
+    double t1 = kNone, t2 = kNone;  // lane g's: the two largest of group g
+    if (lane < a.groups)
+#pragma unroll 4
+      for (int i = 0; i < gs; ++i) {
+        const double v = values[lane * gs + i];
+        t2 = max(t2, min(t1, v));
+        t1 = max(t1, v);
+      }
+    double mine = gs > 1 ? t1 + t2 : t1;
+    if (!(mine == mine)) mine = kNone;
+    allowed = 0;
+    bool free_group = lane < a.groups;
+    for (int g = 0; g < a.top_groups; ++g) {
+      const int at = best_over(free_group ? mine : kNone, free_group ? lane : INT32_MAX);
+      allowed |= 1u << at;
+      if (lane == at) free_group = false;
+    }
+    if (!a.bias) {                  // ordered by the logit
+      wave_lds();
+      for (int e = lane; e < a.E; e += 64) {
+        const double l = value_at<F32>(a.logits, row + e);
+        values[e] = l == l ? l : kNone;
+      }
+      wave_lds();
+    }
+  }
+  uint32_t taken = 0;               // the lane's experts that cannot be chosen (any more)
+  for (int i = 0; i * 64 < a.E; ++i) {
+    const int e = i * 64 + lane;
+    if (e >= a.E || (a.groups > 1 && !(allowed >> (e / gs) & 1))) taken |= 1u << i;
+  }
+  int id = -1;                      // lane j's: the token's j-th expert
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) {
+    double best = kNone;
+    int at = INT32_MAX;
+#pragma unroll 1
+    for (int i = 0; i * 64 < a.E; ++i) {        // a lane's experts rise with i: the first of equals stays
+      const int e = i * 64 + lane;
+      if (taken >> i & 1) continue;
+      const double v = values[e];
+      if (v > best || at == INT32_MAX) best = v, at = e;
+    }
+    at = best_over(best, at);
+    if ((at & 63) == lane) taken |= 1u << (at >> 6);
+    if (lane == j) id = at;
+  }
+  put_choice<64, F32>(a, t, lane, id, true, top, sum, hist);
+}
+
+// Routes one part of the tokens, L lanes a token, lane l holding experts 4 l to
+// 4 l + 3 of every 4 L (so loads are 16 bytes and a group of experts is whole
+// fours).
+//
+// Scores are computed in fp32 with a bound on their error.  The k-th largest of
+// the lanes' maxima is not above the token's k-th largest value; what reaches it
+// within the bound, a dozen values as a rule, goes into a list, and an entry's
+// place is the number of entries before it.  Where two entries lie closer than the
+// bound, places are taken from the list's values in 64 bits, and so are the groups
+// where the last taken and the first that is not lie so close; where more than 32
+// values reach the list or something is not finite, the token is routed again by
+// the whole wave in 64 bits: the choice is always the definition's.  Without bias
+// values are the logits themselves and nothing is uncertain.
+// 16384 tokens, 256 experts in 8 groups with bias: 88 us with everything in 64 bits
+// and a round over all values for each choice, 20 this way (bound by the
+// instructions of about 2000 cycles a wave and by their first fetch).
+constexpr int kRouteList = 32;
+// A value and its expert as one number that is compared: larger values first, the
+// lower number first among equals.
+__device__ __forceinline__ int64_t route_key(float v, int e) {
+  const int bits = __builtin_bit_cast(int, v + 0.0f);          // no -0
+  return (int64_t)((uint64_t)(uint32_t)(bits ^ (bits >> 31 & 0x7fffffff)) << 32 | (uint32_t)~e);
+}
+__device__ __forceinline__ float key_value(int64_t key) {
+  const int bits = (int)(key >> 32);
+  return __builtin_bit_cast(float, bits ^ (bits >> 31 & 0x7fffffff));
+}
+__device__ __forceinline__ int key_expert(int64_t key) { return ~(int)(uint32_t)key; }
+template <int L, int V>
+struct ChoiceLds {
+  static constexpr int kValues = L == 64 ? L * V : V == 4 ? 128 : 32 * V;     // 64 V / 4 pairs, 64 / L lists, E
+  static_assert(kValues >= 32 * V && kValues >= 64 / L * kRouteList && kValues >= L * V, "values of a wave");
+  double values[kRouteWaves][kValues];            // also: the two largest of each four experts of the wave's tokens
+  int64_t list[kRouteWaves][64 / L * kRouteList];
+  int64_t sorted[kRouteWaves][64 / L * kRouteList];
+};
+typedef f32x4_t f32x4a4_t __attribute__((aligned(4)));      // the bias lies at any float
+template <int L, int V>
+union RouteLds {
+  ChoiceLds<L, V> choice;
+  OrderLds order;
+};
+
+// Which groups are taken: lane g's `in` for group g, the least sum taken and the
+// largest that is not.  quads: LDS, the two largest of each four experts.
+template <int L, class T>
+__device__ __forceinline__ void choose_groups(const RouteArgs& a, const T (*quads)[2], int li, bool& in, T& worst,
+                                              T& next) {
+  const T none = -(T)__builtin_huge_val();
+  wave_lds();
+  T t1 = none, t2 = none;
+  const int n = a.E / a.groups / 4;
+  if (li < a.groups)
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      T o[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = li * n + min(i0 + i, n - 1);
+        o[i][0] = quads[q][0];
+        o[i][1] = quads[q][1];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i0 + i < n) {
+          t2 = max(min(t1, o[i][0]), max(t2, o[i][1]));
+          t1 = max(t1, o[i][0]);
+        }
+    }
+  T mine = t1 + t2;
+  if (!(li < a.groups && mine == mine)) mine = none;
+  int place = 0;
+  each_lane<16>(L == 16 ? mine : __shfl(mine, li & 15), [&](int g, T o) { place += o > mine || (o == mine && g < li); });
+  in = li < a.groups && place < a.top_groups;
+  worst = min_over<L>(in ? mine : -none);
+  next = max_over<L>(in ? none : mine);
+}
+
 template <int L, int V, int F32>
 __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs args) {
   (void)args;
   const RouteArgs& a = kernarg<RouteArgs>();
-  __shared__ int hist[kExpertMaxE + 1];
-  __shared__ uint16_t order_ids[kOrderSlots];
-  const int b = blockIdx.x, lane = threadIdx.x & 63, li = lane & (L - 1);
+  __shared__ RouteLds<L, V> lds;
+  __shared__ int hist[kExpertMaxE];
+  constexpr int TOKENS = 64 / L, LIST = kRouteList;
+  constexpr float kLog2e = 1.44269504089f;
+  const int b = blockIdx.x, wave = threadIdx.x >> 6;
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads) hist[e] = 0;
   __syncthreads();
-  constexpr int PASS = kRouteThreads / L;
+  const bool softmax = a.score == SCORE_SOFTMAX, scores = a.bias || a.groups > 1;
+  const int gs = a.E / a.groups, gs_inv = ((1 << 20) + gs - 1) / gs;
+  const bool fours = a.E % 4 == 0 && (a.groups == 1 || gs % 4 == 0);
+  // Twice the largest error of an fp32 value v is below bound (1 + |v|): sigmoid 4e-7 (exp2, reciprocal and sum
+  // round by 1.2e-7 at most, the argument's rounding counts s (1 - s) |x| 2^-24), softmax 2.4e-6 (a sum of 1024).
+  const float bound = !a.bias ? 0.0f : softmax ? 0x1p-17f : 0x1p-20f;
+  const float gbound = softmax ? 0x1p-16f : 0x1p-19f;
   const int t_end = min(a.T, (b + 1) * a.chunk);
-  for (int t0 = b * a.chunk; t0 < t_end; t0 += PASS) {
-    const int t = t0 + (int)threadIdx.x / L;
+  for (int t0 = b * a.chunk + wave * TOKENS; t0 < t_end; t0 += kRouteWaves * TOKENS) {
+    // Hidden from the compiler, which would hold what follows from the lane's number in registers over the loop.
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int li = lane & (L - 1), lt = lane / L, lane0 = lane & ~(L - 1);
+    double(*quads)[2] = reinterpret_cast<double(*)[2]>(lds.choice.values[wave]) + lt * (L * V / 4);
+    int64_t* list = lds.choice.list[wave] + lt * LIST;
+    int64_t* sorted = lds.choice.sorted[wave] + lt * LIST;
+    // Number of the lane's q-th four: turned from q to q, so that groups of experts spread over the lanes.
+    const auto four = [&](int q) { return q * L + ((li + q * (L / 4)) & (L - 1)); };
+    const int t = t0 + lt;
     const bool routed = t < t_end && (!a.mask || a.mask[t]);
-    const int64_t row = (int64_t)(t < t_end ? t : t0) * a.E;
-    float x[V];
-    double v[V];
-    double top = kNone;
+    const int64_t row = (int64_t)min(t, t_end - 1) * a.E;
+    bool unsure = !fours;
+    int id = -1;
+    double top64 = kNone, sum64 = 1.0;
+    if (fours) {
+      float x[V], v[V];
+      float top = -__builtin_huge_valf();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = i * L + li;
-      x[i] = e < a.E ? value_at<F32>(a.logits, row + e) : -__builtin_huge_valf();
-      v[i] = x[i];
-      top = fmax(top, v[i]);
-    }
-    if (a.score == SCORE_SOFTMAX) top = max_over<L>(top);
-    double sum = 1.0;
-    const bool scores = a.bias || a.groups > 1;
-    if (a.score == SCORE_SOFTMAX && (scores || !a.renorm)) {
-      sum = 0.0;
+      for (int q = 0; q < V / 4; ++q) {
+        const int e = four(q) * 4;
+        f32x4_t w = f32x4_t{top, top, top, top};       // past the last expert: -inf
+        if (e < a.E) {
+          if constexpr (F32) {
+            w = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(a.logits) + row + e);
+          } else {
+            const u32x2_t h = *reinterpret_cast<const u32x2_t*>(reinterpret_cast<const uint16_t*>(a.logits) + row + e);
+            w = f32x4_t{__uint_as_float(h[0] << 16), __uint_as_float(h[0] & 0xffff0000u), __uint_as_float(h[1] << 16),
+                        __uint_as_float(h[1] & 0xffff0000u)};
+          }
+        }
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += top == kNone ? 0.0 : exp((double)x[i] - top);
-      sum = sum_over<L>(sum);
-    }
-    uint32_t taken = 0;               // the lane's experts that cannot be chosen (any more)
+        for (int i = 0; i < 4; ++i) x[4 * q + i] = w[i];
+      }
+      bool lost = false;            // to be routed in 64 bits
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i * L + li >= a.E) taken |= 1u << i;
-    if (scores) {
-      double biased[V];
+      for (int i = 0; i < V; ++i) lost |= !(x[i] == x[i]);
+      if (softmax) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = i * L + li;
-        const double s = a.score == SCORE_SIGMOID ? 1.0 / (1.0 + exp(-(double)x[i]))
-                                                  : (top == kNone ? 0.0 : exp((double)x[i] - top) / sum);
-        biased[i] = s + (a.bias && e < a.E ? (double)a.bias[e] : 0.0);
-        if (!(biased[i] == biased[i])) biased[i] = kNone;
-        if (a.bias) v[i] = biased[i];
+        for (int i = 0; i < V; ++i) top = max(top, x[i]);
+        top = max_over<L>(top);
+        lost |= !(fabsf(top) < __builtin_huge_valf());
+        top64 = top;
+        if (!a.renorm) sum64 = softmax_sum<L, F32>(a, row, li, top64);
+      }
+      if (scores) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          v[i] = __builtin_amdgcn_exp2f((softmax ? x[i] - top : -x[i]) * kLog2e);
+          if (softmax) sum += v[i];
+        }
+        const float inv = softmax ? __builtin_amdgcn_rcpf(sum_over<L>(sum)) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = softmax ? v[i] * inv : __builtin_amdgcn_rcpf(1.0f + v[i]);
+        if (a.bias)
+#pragma unroll
+          for (int q = 0; q < V / 4; ++q)
+            if (four(q) * 4 < a.E) {
+              const f32x4a4_t c = *reinterpret_cast<const f32x4a4_t*>(a.bias + four(q) * 4);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[4 * q + i] += c[i];
+            }
       }
       if (a.groups > 1) {
-        const int gs = a.E / a.groups;
-        double mine = kNone;          // lane g's: the sum of the two largest of group g
-        for (int g = 0; g < a.groups; ++g) {
-          double t1 = kNone, t2 = kNone;
+        bool in;
+        float worst, next;
+        float(*pairs)[2] = reinterpret_cast<float(*)[2]>(quads);
+        wave_lds();
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int e = i * L + li;
-            if (e >= g * gs && e < (g + 1) * gs) {
-              t2 = fmax(t2, fmin(t1, biased[i]));
-              t1 = fmax(t1, biased[i]);
+        for (int q = 0; q < V / 4; ++q) {
+          const float a0 = max(v[4 * q], v[4 * q + 1]), a1 = min(v[4 * q], v[4 * q + 1]);
+          const float b0 = max(v[4 * q + 2], v[4 * q + 3]), b1 = min(v[4 * q + 2], v[4 * q + 3]);
+          pairs[four(q)][0] = max(a0, b0);
+          pairs[four(q)][1] = max(min(a0, b0), max(a1, b1));
+        }
+        choose_groups<L>(a, pairs, li, in, worst, next);
+        if (__ballot(a.top_groups < a.groups && !(worst - next > gbound * (1.0f + fabsf(worst))))) {
+          if (softmax && a.renorm) sum64 = softmax_sum<L, F32>(a, row, li, top64);
+          double worst64, next64;
+          wave_lds();
+#pragma unroll 1
+          for (int q = li; q < a.E / 4; q += L) {
+            double t1 = kNone, t2 = kNone;
+#pragma unroll 1
+            for (int e = q * 4; e < q * 4 + 4; ++e) {
+              const double l = value_at<F32>(a.logits, row + e);
+              const double s = (softmax ? exp(l - top64) / sum64 : sigmoid64(l)) + (a.bias ? (double)a.bias[e] : 0.0);
+              t2 = max(t2, min(t1, s));
+              t1 = max(t1, s);
             }
+            quads[q][0] = t1;
+            quads[q][1] = t2;
           }
-#pragma unroll
-          for (int d = 1; d < L; d <<= 1) {
-            const double o1 = __shfl_xor(t1, d), o2 = __shfl_xor(t2, d);
-            t2 = fmax(fmin(t1, o1), fmax(t2, o2));
-            t1 = fmax(t1, o1);
-          }
-          if (li == g) mine = gs > 1 ? t1 + t2 : t1;
+          choose_groups<L>(a, quads, li, in, worst64, next64);
         }
-        if (!(mine == mine)) mine = kNone;
-        uint32_t allowed = 0;
-        bool free_group = li < a.groups;
-        for (int g = 0; g < a.top_groups; ++g) {
-          const int at = best_over<L>(free_group ? mine : kNone, free_group ? li : INT32_MAX);
-          allowed |= 1u << at;
-          if (li == at) free_group = false;
-        }
+        const uint32_t allowed = (uint32_t)(__ballot(in) >> lane0) & 0xffffu;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (!(allowed >> min((i * L + li) / gs, 31) & 1)) taken |= 1u << i;
+        for (int q = 0; q < V / 4; ++q) {
+          const int g = (int)((uint32_t)(four(q) * 4) * (uint32_t)gs_inv >> 20);
+          const bool in = g < a.groups && (allowed >> g & 1);
+#pragma unroll
+          for (int i = 4 * q; i < 4 * q + 4; ++i) v[i] = in ? (a.bias ? v[i] : x[i]) : -__builtin_huge_valf();
+        }
+      } else if (!a.bias) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = x[i];
+      } else {
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q)
+          if (four(q) * 4 >= a.E)
+#pragma unroll
+            for (int i = 4 * q; i < 4 * q + 4; ++i) v[i] = -__builtin_huge_valf();
       }
-    }
+      // The k-th largest of the lanes' maxima.
+      float m = v[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!(v[i] == v[i])) v[i] = kNone;
-    int id = -1;                      // lane j's: the token's j-th expert
-    for (int j = 0; j < a.k; ++j) {
-      double best = kNone;
-      int at = INT32_MAX;
+      for (int i = 1; i < V; ++i) m = max(m, v[i]);
+      int place = 0;
+      each_lane<L>(m, [&](int j, float o) { place += o > m || (o == m && j < li); });
+      const uint64_t kth = __ballot(place == a.k - 1) >> lane0 & (L == 64 ? ~0ull : (1ull << L) - 1);
+      float least = __shfl(m, lane0 + (kth ? __builtin_ctzll(kth) : 0));
+      least -= 2.0f * bound * (1.0f + fabsf(least));
+      lost |= !(least > -__builtin_huge_valf());
+      int n = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i)     // a lane's experts rise with i: the first of equals stays
-        if (!(taken >> i & 1) && (v[i] > best || at == INT32_MAX)) best = v[i], at = i * L + li;
-      at = best_over<L>(best, at);
+      for (int i = 0; i < V; ++i) n += v[i] >= least;
+      const int upto = sum_upto<L>(n, li);
+      const int total = max_over<L>(upto);
+      lost |= total > LIST;
+      int at = upto - n;
+      wave_lds();
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i * L + li == at) taken |= 1u << i;
-      if (li == j) id = at;
+        if (v[i] >= least) {
+          if (at < LIST) list[at] = route_key(v[i], four(i / 4) * 4 + i % 4);
+          ++at;
+        }
+      wave_lds();
+      const int held = min(total, LIST);
+      int most = held;
+#pragma unroll
+      for (int d = L; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+      most = __builtin_amdgcn_readfirstlane(most);
+      // Entries li and (where 16 lanes share the token) li + 16: their places.
+      constexpr int PER = LIST > L ? LIST / L : 1;
+      int64_t own[PER];
+      int before[PER] = {};
+#pragma unroll
+      for (int i = 0; i < PER; ++i) own[i] = list[min(li + i * L, LIST - 1)];
+      for (int j0 = 0; j0 < most; j0 += 4) {
+        int64_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = list[j0 + j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < PER; ++i) before[i] += j0 + j < held && o[j] > own[i];
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (li + i * L < held) sorted[before[i]] = own[i];
+      wave_lds();
+      bool close = false;           // lane j: entry j and the one after it
+      if (a.bias && li < a.k && li + 1 < held) {
+        const float v0 = key_value(sorted[li]), v1 = key_value(sorted[li + 1]);
+        close = !(v0 - v1 > bound * (1.0f + fabsf(v0)));
+      }
+      if (__ballot(close)) {        // places by the values in 64 bits
+        if (softmax && a.renorm) sum64 = softmax_sum<L, F32>(a, row, li, top64);
+        double* values = lds.choice.values[wave] + lt * LIST;
+#pragma unroll 1
+        for (int j = li; j < held; j += L) {
+          const int e = key_expert(list[j]);
+          const double l = value_at<F32>(a.logits, row + e);
+          values[j] = (softmax ? exp(l - top64) / sum64 : sigmoid64(l)) + (double)a.bias[e];
+        }
+        wave_lds();
+#pragma unroll 1
+        for (int i = li; i < held; i += L) {
+          const double mine = values[i];
+          const int64_t key = list[i];
+          int n = 0;
+#pragma unroll 1
+          for (int j = 0; j < held; ++j) n += values[j] > mine || (values[j] == mine && key_expert(list[j]) < key_expert(key));
+          sorted[n] = key;
+        }
+        wave_lds();
+      }
+      if (li < a.k) id = key_expert(sorted[li]);
+      unsure = (__ballot(lost) >> lane0 & (L == 64 ? ~0ull : (1ull << L) - 1)) != 0;
     }
-    const bool mine = routed && li < a.k && (uint32_t)id < (uint32_t)a.E;
-    double s = 0.0;
-    if (mine) {
-      const double l = value_at<F32>(a.logits, row + id);
-      s = a.score == SCORE_SIGMOID ? 1.0 / (1.0 + exp(-l)) : (top == kNone ? 0.0 : exp(l - top));
-    }
-    if (a.renorm) sum = sum_over<L>(s);
-    if (t < t_end && li < a.k) {
-      double w = 0.0;
-      if (mine) w = a.renorm ? (sum == 0.0 ? 0.0 : a.scale * (s / sum)) :
-                    a.scale * (a.score == SCORE_SIGMOID || sum == 0.0 ? s : s / sum);
-      a.ids[(int64_t)t * a.k + li] = mine ? id : -1;
-      a.weights[(int64_t)t * a.k + li] = (float)w;
-      if (mine) atomicAdd(&hist[id], 1);
+    if (t < t_end && !(unsure && routed)) put_choice<L, F32>(a, t, li, id, routed, top64, sum64, hist);
+    uint64_t again = __ballot(unsure && routed && li == 0);
+    while (again) {
+      const int at = __builtin_ctzll(again);
+      again &= again - 1;
+      route_token<F32>(a, __builtin_amdgcn_readlane(t, at), lane, hist, lds.choice.values[wave]);
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.hist[(int64_t)b * a.E + e] = hist[e];
   if (a.chunks == 1) {
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) lds.order.base[e] = hist[e];
     __syncthreads();
-    order_part(a, 0, hist, order_ids);
+    order_part(a, 0, lds.order);
+  } else {
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) a.hist[(int64_t)e * a.pad + b] = (uint16_t)hist[e];
   }
 }
 
-// The router's gradient: one wave a token, lane l holding the experts l, l + 64, ...
-// Through renormalised weights w = c s / sum s:  dl = w (dw - sum_i w_i dw_i / c),
-// times 1 - s for sigmoid scores; otherwise through w = c s.
+// The router's gradient.  Through renormalised weights w = c s / sum s it is
+// dl = w (dw - sum_i w_i dw_i / c), times 1 - s for sigmoid scores; otherwise
+// dl = w dw (1 - s) through w = c s of a sigmoid: nothing but the chosen experts'
+// logits matter.  16 lanes take a token's choices and lay its row out in LDS.
+constexpr int kGradTokens = 16;
 template <int F32>
 __global__ __launch_bounds__(256) void expert_route_backward_kernel(RouteGradArgs args) {
+  (void)args;
+  const RouteGradArgs& a = kernarg<RouteGradArgs>();
+  extern __shared__ __attribute__((aligned(16))) float rows[];      // [kGradTokens][E rounded up to 8]
+  const int lane = threadIdx.x & 63, li = lane & 15, tok = threadIdx.x >> 4, width = (a.E + 7) & ~7;
+  float* mine = rows + tok * width;
+  for (int64_t t0 = (int64_t)blockIdx.x * kGradTokens; t0 < a.T; t0 += (int64_t)gridDim.x * kGradTokens) {
+    const int64_t t = t0 + tok;
+    for (int e = li * 4; e < width; e += 64) *reinterpret_cast<f32x4_t*>(mine + e) = f32x4_t{0, 0, 0, 0};
+    int id = -1;
+    double w = 0.0, g = 0.0;
+    if (t < a.T && li < a.k) {
+      id = a.ids[t * a.k + li];
+      if ((uint32_t)id >= (uint32_t)a.E) id = -1;
+      if (id >= 0) {
+        w = a.weights[t * a.k + li];
+        g = a.dweights[t * a.k + li];
+      }
+    }
+    const double total = sum_over<16>(w * g);
+    double d = a.renorm ? w * (g - total / a.scale) : w * g;
+    if (a.score == SCORE_SIGMOID && id >= 0) d = d / (1.0 + exp((double)value_at<F32>(a.logits, t * a.E + id)));
+    wave_lds();
+    if (id >= 0) mine[id] = (float)d;
+    wave_lds();
+    if (t < a.T && a.E % 8 == 0) {                        // rows of the gradient are whole 16 bytes
+      for (int e = li * 8; e < a.E; e += 128) {
+        const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(mine + e);
+        const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(mine + e + 4);
+        if constexpr (F32) {
+          f32x4_t* out = reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.dlogits) + t * a.E + e);
+          out[0] = lo;
+          out[1] = hi;
+        } else {
+          *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.dlogits) + t * a.E + e) =
+              u32x4_t{bf16_pair(lo[0], lo[1]), bf16_pair(lo[2], lo[3]), bf16_pair(hi[0], hi[1]), bf16_pair(hi[2], hi[3])};
+        }
+      }
+    } else if (t < a.T) {
+      for (int e = li; e < a.E; e += 16) {
+        if constexpr (F32) reinterpret_cast<float*>(a.dlogits)[t * a.E + e] = mine[e];
+        else reinterpret_cast<uint16_t*>(a.dlogits)[t * a.E + e] = (uint16_t)f32_to_bf16_bits(mine[e]);
+      }
+    }
+    wave_lds();
+  }
+}
+
+// Through softmax scores that are not renormalised every logit has a gradient:
+// dl = s (g - sum_i s_i g_i), g = c dw at the chosen, 0 elsewhere.  One wave a token.
+template <int F32>
+__global__ __launch_bounds__(256) void expert_route_dense_backward_kernel(RouteGradArgs args) {
   (void)args;
   const RouteGradArgs& a = kernarg<RouteGradArgs>();
   const int lane = threadIdx.x & 63;
   for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += (int64_t)gridDim.x * 4) {
     const int64_t row = t * a.E;
     int id = -1;
-    double d = 0.0, w = 0.0, g = 0.0;
+    double d = 0.0;
     if (lane < a.k) {
       id = a.ids[t * a.k + lane];
       if ((uint32_t)id >= (uint32_t)a.E) id = -1;
-      if (id >= 0) {
-        w = a.weights[t * a.k + lane];
-        g = a.dweights[t * a.k + lane];
-      }
+      if (id >= 0) d = (double)a.weights[t * a.k + lane] * a.dweights[t * a.k + lane];
     }
     const bool routed = __ballot(id >= 0) != 0;
-    const bool dense = a.score == SCORE_SOFTMAX && !a.renorm;
-    const double l = id >= 0 ? (double)value_at<F32>(a.logits, row + id) : 0.0;
-    const double total = sum_over<64>(w * g);
-    if (id >= 0) {
-      if (a.renorm) {
-        d = w * (g - total / a.scale);
-        if (a.score == SCORE_SIGMOID) d = d / (1.0 + exp(l));
-      } else if (a.score == SCORE_SIGMOID) {
-        d = w * g / (1.0 + exp(l));
-      } else {
-        d = w * g;
-      }
-    }
+    const double total = sum_over<64>(d);
     const float df = (float)d;
     double top = kNone, sum = 0.0;
-    if (dense && routed) {
-      for (int e = lane; e < a.E; e += 64) top = fmax(top, (double)value_at<F32>(a.logits, row + e));
+    if (routed) {
+      for (int e = lane; e < a.E; e += 64) top = max(top, (double)value_at<F32>(a.logits, row + e));
       top = max_over<64>(top);
       for (int e = lane; e < a.E; e += 64) sum += exp((double)value_at<F32>(a.logits, row + e) - top);
       sum = sum_over<64>(sum);
@@ -300,7 +727,7 @@ __global__ __launch_bounds__(256) void expert_route_backward_kernel(RouteGradArg
         if (e == ej) out = dj;
       }
       if (e < a.E) {
-        if (dense && routed && top != kNone) out -= (float)(exp((double)value_at<F32>(a.logits, row + e) - top) / sum * total);
+        if (routed && top != kNone) out -= (float)(exp((double)value_at<F32>(a.logits, row + e) - top) / sum * total);
         if (F32) reinterpret_cast<float*>(a.dlogits)[row + e] = out;
         else reinterpret_cast<uint16_t*>(a.dlogits)[row + e] = (uint16_t)f32_to_bf16_bits(out);
       }
@@ -334,7 +761,7 @@ __device__ __forceinline__ void store8(void* p, int64_t at, const float (&v)[8])
   } else {
     u32x4_t w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_bits(v[2 * i]) | f32_to_bf16_bits(v[2 * i + 1]) << 16;
+    for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(p) + at) = w;
   }
 }
@@ -433,8 +860,9 @@ hipError_t launch_route_sized(const RouteArgs& a, hipStream_t s) {
 }  // namespace
 
 int route_chunks(int64_t T, int64_t* chunk) {
-  int64_t c = (T + 255) / 256;                              // at most 256 parts
+  int64_t c = (T + 255) / 256;                              // 256 parts, one a compute unit
   c = std::max<int64_t>(kRouteTokens, (c + kRouteTokens - 1) / kRouteTokens * kRouteTokens);
+  c = std::min<int64_t>(c, 1023 * kRouteTokens);            // a part's counts are held in 16 bits
   if (chunk) *chunk = c;
   return (int)((T + c - 1) / c);
 }
@@ -450,9 +878,16 @@ hipError_t launch_expert_route(const RouteArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_expert_route_backward(const RouteGradArgs& a, hipStream_t s) {
-  const unsigned blocks = (unsigned)std::min<int64_t>(((int64_t)a.T + 3) / 4, 1 << 20);
-  if (a.logits_f32) hipLaunchKernelGGL(expert_route_backward_kernel<1>, dim3(blocks), dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(expert_route_backward_kernel<0>, dim3(blocks), dim3(256), 0, s, a);
+  if (a.score == SCORE_SOFTMAX && !a.renorm) {
+    const unsigned blocks = (unsigned)std::min<int64_t>(((int64_t)a.T + 3) / 4, 1 << 20);
+    if (a.logits_f32) hipLaunchKernelGGL(expert_route_dense_backward_kernel<1>, dim3(blocks), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(expert_route_dense_backward_kernel<0>, dim3(blocks), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  const unsigned blocks = (unsigned)std::min<int64_t>(((int64_t)a.T + kGradTokens - 1) / kGradTokens, 1 << 22);
+  const unsigned lds = kGradTokens * ((a.E + 7) / 8 * 8) * sizeof(float);      // at most 64 KiB
+  if (a.logits_f32) hipLaunchKernelGGL(expert_route_backward_kernel<1>, dim3(blocks), dim3(256), lds, s, a);
+  else hipLaunchKernelGGL(expert_route_backward_kernel<0>, dim3(blocks), dim3(256), lds, s, a);
   return hipGetLastError();
 }
 

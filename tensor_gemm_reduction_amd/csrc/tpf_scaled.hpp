@@ -17,6 +17,13 @@ constexpr int kExpertMaxGroups = 16;
 
 enum ScoreKind : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
 
+// Two values rounded to bf16 (nearest even), the first in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const bf16x2_t v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 constexpr int64_t scale_blocks(int64_t n) { return (n + kScaleBlock - 1) / kScaleBlock; }
 // Scale bytes of a packed row of n values: whole words, so that one word load
 // brings four blocks' scales.
@@ -83,12 +90,12 @@ struct RouteArgs {
   int* offsets;                      // [E + 1]
   int* src;                          // [T k]
   int* pos;                          // [T][k]
-  int* hist;                         // [chunks][E]
+  uint16_t* hist;                    // [E][pad]: rows of each expert in each part
   int T, E, k;
   int score, groups, top_groups, renorm;
   double scale;
   int logits_f32;
-  int chunks, chunk;                 // parts of the tokens, tokens in each
+  int chunks, chunk, pad;            // parts of the tokens, tokens in each; chunks rounded up to 4
 };
 // Parts that T tokens are cut into: each counts its experts' rows by itself.
 int route_chunks(int64_t T, int64_t* chunk);

@@ -294,7 +294,7 @@ int tpf_expert_weight_grad(tpf_handle h, int p, int64_t Mt, int64_t R, int64_t C
 
 size_t tpf_expert_route_ws(int64_t T, int64_t E) {
   if (T < 1 || T > INT32_MAX || E < 1 || E > kExpertMaxE) return 0;
-  return (size_t)route_chunks(T, nullptr) * (size_t)E * sizeof(int);
+  return (size_t)((route_chunks(T, nullptr) + 3) / 4 * 4) * (size_t)E * sizeof(uint16_t);
 }
 
 int tpf_expert_route(tpf_handle h, int64_t T, int64_t E, int k, const void* logits, int dtype, int score,
@@ -326,7 +326,7 @@ int tpf_expert_route(tpf_handle h, int64_t T, int64_t E, int k, const void* logi
     a.offsets = offsets;
     a.src = src;
     a.pos = pos;
-    a.hist = reinterpret_cast<int*>(ws);
+    a.hist = reinterpret_cast<uint16_t*>(ws);
     a.T = (int)T;
     a.E = (int)E;
     a.k = k;
@@ -339,6 +339,7 @@ int tpf_expert_route(tpf_handle h, int64_t T, int64_t E, int k, const void* logi
     int64_t chunk;
     a.chunks = route_chunks(T, &chunk);
     a.chunk = (int)chunk;
+    a.pad = (a.chunks + 3) / 4 * 4;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     TPF_TIMED(h, s, launch_expert_route(a, s));
     return TPF_OK;

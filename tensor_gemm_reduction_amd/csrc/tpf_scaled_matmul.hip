@@ -345,8 +345,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void scaled_tile_kernel(ScaledArgs ar
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rs, off, 0, 0);
       else
         __builtin_amdgcn_raw_buffer_store_b64(
-            u32x2_t{f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
-                    f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16}, rs, off, 0, 0);
+            u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}, rs, off, 0, 0);
     }
 }
 
