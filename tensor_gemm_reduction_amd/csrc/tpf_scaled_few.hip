@@ -1,0 +1,196 @@
+// Products of 8-bit operands for a few rows (a decode step): the weights are
+// streamed once from memory into registers.
+//
+// A workgroup owns 16 TM rows and 16 TN columns of the result; its W waves take
+// the blocks of 128 along the contraction (and over the shards) in turn, each U of
+// its own ahead, and their sums are joined in LDS in the order of the waves.
+// A lane's 32 codes of a block are two 16-byte loads of one weight row, so four
+// lanes read whole 64-byte halves of its 128.  Codes become bf16 (exact) and go to
+// the bf16 instructions, whose sums keep fp32's bits: next to memory the
+// conversions are small (192 cycles of a SIMD's 1260 that a block's 4 KB take at
+// 8 TB/s).
+#include <algorithm>
+
+#include "tpf_gemm.hpp"
+#include "tpf_scaled.hpp"
+#include "tpf_scaled_device.hpp"
+
+namespace tpf {
+namespace {
+
+// U: loads of about 8 KB a wave in flight, as the registers allow.
+constexpr int few_ahead(int TM) { return TM == 1 ? 4 : TM == 2 ? 3 : 2; }
+
+template <int TM, int TN>
+struct FewBlock {
+  i32x8_t x[TM], w[TN];
+  int xs[TM];
+  float ws;
+};
+
+template <int TM, int TN, int W, int EXPERTS, int WS, int OUT>
+__global__ __launch_bounds__(64 * W) void scaled_few_kernel(ScaledArgs args) {
+  (void)args;
+  const ScaledArgs& a = *(const ScaledArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  __shared__ f32x4_t part[W][TM * TN][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = blockIdx.x / a.tiles_n, n0 = (int)(blockIdx.x - unit * a.tiles_n) * 16 * TN;
+  int e = 0, row0 = unit * 16 * TM, rows = min(16 * TM, a.M - row0);
+  const int kbs = (a.K + kScaleBlock - 1) / kScaleBlock;
+  int blocks = a.p * kbs;
+  if constexpr (EXPERTS) {
+    const RowTile t = expert_tile<16 * TM>(a.offsets, a.E, a.M, unit, lane);
+    if (t.rows <= 0) return;
+    row0 = t.row0;
+    rows = t.rows;
+    e = t.e;
+    if (e == a.E) e = 0, blocks = 0;                 // rows of no expert: zeros
+  }
+  // This lane's rows of both operands, as offsets from the first (of gathered rows: from the first token); rows and
+  // columns past the last repeat it and are not stored.
+  constexpr int U = few_ahead(TM);
+  const int r16 = lane & 15, chunk = 16 * (lane >> 4);
+  const bool gather = EXPERTS && a.top;
+  uint32_t x_at[TM], w_at[TN], xs_at[TM];
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    int r = min(m * 16 + r16, rows - 1);
+    if (gather) r = min(max(a.src[row0 + r], 0) / a.top, a.xrows - 1);
+    x_at[m] = (uint32_t)r * (uint32_t)a.K + chunk;
+    xs_at[m] = (uint32_t)r * (uint32_t)a.xsw;
+  }
+#pragma unroll
+  for (int n = 0; n < TN; ++n) w_at[n] = (uint32_t)min(n * 16 + r16, a.N - 1 - n0) * (uint32_t)a.K + chunk;
+  const int64_t x_row = gather ? 0 : row0, w_row = (int64_t)e * a.N + n0;
+  const int64_t x_bytes = (int64_t)(gather ? a.xrows : rows) * a.K, w_bytes = (int64_t)min(16 * TN, a.N - n0) * a.K;
+  const int64_t ws_at = ((int64_t)e * ((a.N + kScaleBlock - 1) / kScaleBlock) + n0 / kScaleBlock) * a.wsw;
+
+  // The next block to be loaded.  Tiles start at blocks of their own: from the same one, rows whose length is a power
+  // of two would all be read from the same few memory channels.
+  const int b0 = blocks ? (int)((uint32_t)(wave + (n0 / (16 * TN) + unit) * W) % (uint32_t)blocks) : 0;
+  int s = b0 / kbs, kb = b0 - s * kbs;
+  const auto load = [&](FewBlock<TM, TN>& b) {
+    const int k0 = kb * kScaleBlock;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x[s] + x_row * a.K, x_bytes), rw = make_rsrc(a.w[s] + w_row * a.K, w_bytes);
+    // codes past the end of a row read as zeros
+    const bool tail = k0 + kScaleBlock > a.K;
+    const uint32_t lo = tail && k0 + chunk >= a.K ? kOOB : 0, hi = tail && k0 + chunk + 64 >= a.K ? kOOB : 0;
+    const auto codes = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t at) {
+      const i32x4_t c0 = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(at | lo), k0, 0));
+      const i32x4_t c1 = __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)((at + 64) | hi), k0, 0));
+      return __builtin_shufflevector(c0, c1, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+#pragma unroll
+    for (int n = 0; n < TN; ++n) b.w[n] = codes(rw, w_at[n]);
+#pragma unroll
+    for (int m = 0; m < TM; ++m) b.x[m] = codes(rx, x_at[m]);
+    const uint8_t* xs = a.xs[s] + x_row * a.xsw + kb;
+#pragma unroll
+    for (int m = 0; m < TM; ++m) b.xs[m] = xs[xs_at[m]];
+    if constexpr (WS == WS_F32) b.ws = reinterpret_cast<const float*>(a.ws[s])[ws_at + kb];
+    else b.ws = exp_byte(a.ws[s][ws_at + kb]);
+    kb += W;
+    while (kb >= kbs) {
+      kb -= kbs;
+      if (++s == a.p) s = 0;
+    }
+  };
+  f32x4_t acc[TM][TN];
+#pragma unroll
+  for (int m = 0; m < TM; ++m)
+#pragma unroll
+    for (int n = 0; n < TN; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
+  const int mine = blocks > wave ? (blocks - wave + W - 1) / W : 0;
+  FewBlock<TM, TN> ring[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < mine) load(ring[u]);
+  for (int i = 0; i < mine; i += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u >= mine) break;
+      ScFine w[TN];
+#pragma unroll
+      for (int n = 0; n < TN; ++n) w[n] = sc_fine(ring[u].w[n]);
+#pragma unroll
+      for (int m = 0; m < TM; ++m) {
+        const ScFine x = sc_fine(ring[u].x[m]);
+        const float f = exp_byte(ring[u].xs[m]) * ring[u].ws;
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+          const f32x4_t v = sc_mfma_fine(w[n], x);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[m][n][q] = __builtin_fmaf(v[q], f, acc[m][n][q]);
+        }
+      }
+      if (i + u + U < mine) load(ring[u]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < TM; ++m)
+#pragma unroll
+    for (int n = 0; n < TN; ++n) part[wave][m * TN + n][lane] = acc[m][n];
+  __syncthreads();
+  for (int i = threadIdx.x; i < TM * TN * 64; i += 64 * W) {
+    const int t = i >> 6, l = i & 63;
+    f32x4_t v = part[0][t][l];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += part[w][t][l];
+    const int row = t / TN * 16 + (l & 15), col = n0 + t % TN * 16 + 4 * (l >> 4);
+    if (row >= rows || col >= a.N) continue;
+    if (a.gelu) v = f32x4_t{gelu_f32(v[0]), gelu_f32(v[1]), gelu_f32(v[2]), gelu_f32(v[3])};
+    const int64_t at = (int64_t)(row0 + row) * a.N + col;
+    if constexpr (OUT == OUT_F32)
+      *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.y[0]) + at) = v;
+    else
+      *reinterpret_cast<u32x2_t*>(reinterpret_cast<uint16_t*>(a.y[0]) + at) =
+          u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+  }
+}
+
+template <int TM, int TN, int W, int EXPERTS, int WS>
+hipError_t launch_few(ScaledArgs a, hipStream_t s) {
+  a.tiles_n = (a.N + 16 * TN - 1) / (16 * TN);
+  a.tiles_m = EXPERTS ? expert_tiles(a.M, a.E, 16 * TM) : (a.M + 16 * TM - 1) / (16 * TM);
+  if (a.out == OUT_F32)
+    hipLaunchKernelGGL((scaled_few_kernel<TM, TN, W, EXPERTS, WS, OUT_F32>), dim3(a.tiles_n * a.tiles_m), dim3(64 * W),
+                       0, s, a);
+  else
+    hipLaunchKernelGGL((scaled_few_kernel<TM, TN, W, EXPERTS, WS, OUT_BF16>), dim3(a.tiles_n * a.tiles_m), dim3(64 * W),
+                       0, s, a);
+  return hipGetLastError();
+}
+
+// Four waves a workgroup, so that three workgroups share a compute unit and one's
+// start and end lie beside the others' streams (16 tokens to 8 of 64 experts, K
+// 4096, N 1024: 49 us, with eight waves 62; 1 x 8192 x 8192: 14.8 against 17.4).
+// Eight where they read whole rows of the weights, or where there are few columns
+// (16 x 8 x 1024 x 8192: 15.5 against 16.6).
+template <int TM, int EXPERTS, int WS>
+hipError_t launch_few_sized(const ScaledArgs& a, hipStream_t s) {
+  const int64_t kbs = scale_blocks(a.K);
+  const bool eight = !EXPERTS && a.p * kbs >= 16 && (kbs <= 8 || a.N <= 2048);
+  return eight ? launch_few<TM, 2, 8, EXPERTS, WS>(a, s) : launch_few<TM, 2, 4, EXPERTS, WS>(a, s);
+}
+
+template <int EXPERTS, int WS>
+hipError_t launch_few_rows(const ScaledArgs& a, int tm, hipStream_t s) {
+  if (tm == 1) return launch_few_sized<1, EXPERTS, WS>(a, s);
+  if (tm == 2) return launch_few_sized<2, EXPERTS, WS>(a, s);
+  return launch_few_sized<4, EXPERTS, WS>(a, s);
+}
+
+}  // namespace
+
+int scaled_few_tiles(int64_t M, int64_t E) {
+  const int64_t rows = E ? (M + E - 1) / E : M;      // of an expert, if all get as many
+  if (E) return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 40 ? 4 : 0;
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
+}
+
+hipError_t launch_scaled_few(const ScaledArgs& a, int wscale, int tm, hipStream_t s) {
+  if (a.E) return wscale == WS_F32 ? launch_few_rows<1, WS_F32>(a, tm, s) : launch_few_rows<1, WS_BYTE>(a, tm, s);
+  return wscale == WS_F32 ? launch_few_rows<0, WS_F32>(a, tm, s) : launch_few_rows<0, WS_BYTE>(a, tm, s);
+}
+
+}  // namespace tpf

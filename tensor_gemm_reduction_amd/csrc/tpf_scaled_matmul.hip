@@ -376,6 +376,7 @@ hipError_t launch_mode(const ScaledArgs& a, int64_t rows, int64_t outs, hipStrea
 }  // namespace
 
 hipError_t launch_scaled_matmul(ScaledArgs a, int wscale, hipStream_t s) {
+  if (const int few = scaled_few_tiles(a.M, a.E)) return launch_scaled_few(a, wscale, few, s);
   if (a.E) {
     return wscale == WS_F32 ? launch_mode<EXPERTS, WS_F32>(a, a.M, 1, s) : launch_mode<EXPERTS, WS_BYTE>(a, a.M, 1, s);
   }
