@@ -20,9 +20,9 @@ ARGS = os.path.join(LIBDIR, "_args.so")      # the Python binding's native argum
 
 SOURCES = ["tpf_kernels.hip", "tpf_api.cpp", "tpf_block_api.cpp", "tpf_norm.hip", "tpf_stash.hip",
            "tpf_stash_grad.hip", "tpf_qweight.hip", "tpf_scaled_api.cpp", "tpf_scaled_pack.hip", "tpf_scaled_matmul.hip",
-           "tpf_scaled_few.hip",           "tpf_experts.hip"]
+           "tpf_scaled_few.hip", "tpf_experts.hip"]
 HEADERS = ["tpf_device.hpp", "tpf_internal.hpp", "tpf_gemm.hpp", "tpf_stationary.hpp", "tpf_host.hpp",
-           "tpf_block.hpp", "tpf_tiles.hpp", "tpf_scaled.hpp", "tpf_scaled_device.hpp"]
+           "tpf_block.hpp", "tpf_tiles.hpp", "tpf_scaled.hpp", "tpf_scaled_device.hpp", "tpf_gauss.hpp"]
 
 # Packed-fp32 instructions are disabled for all device code: the compiler
 # would otherwise form v_pk_* fp32 ops from plain float code.

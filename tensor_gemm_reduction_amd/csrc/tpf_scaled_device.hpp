@@ -2,6 +2,7 @@
 // the experts' rows.
 #pragma once
 
+#include "tpf_gauss.hpp"
 #include "tpf_scaled.hpp"
 
 namespace tpf {
@@ -40,6 +41,10 @@ __device__ __forceinline__ f32x4_t sc_mfma_fine(const ScFine& w, const ScFine& x
 #pragma unroll
   for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.k[i], x.k[i], c, 0, 0, 0);
   return c;
+}
+// GeLU, x Phi(x), to a few roundings of fp32.
+__device__ __forceinline__ f32x4_t sc_gelu(f32x4_t v) {
+  return f32x4_t{v[0] * gauss<1>(v[0]).cdf, v[1] * gauss<1>(v[1]).cdf, v[2] * gauss<1>(v[2]).cdf, v[3] * gauss<1>(v[3]).cdf};
 }
 // 2^(e - 127)
 __device__ __forceinline__ float exp_byte(int e) { return e == 0 ? 0x1p-127f : __uint_as_float((uint32_t)e << 23); }

@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "tpf_block.hpp"
+#include "tpf_gauss.hpp"
 
 namespace tpf {
 
@@ -27,52 +28,6 @@ typedef u32x2_t u32x2a4_t __attribute__((aligned(4)));   // codes rows are 8-byt
 template <class A>
 __device__ __forceinline__ const A& stash_kernarg() {
   return *(const A*)__builtin_amdgcn_kernarg_segment_ptr();
-}
-
-// Phi(-a) / exp(-a^2 / 2) for a >= 0 as a polynomial in 1 / (1 + c a), fitted
-// here to the least largest relative error over [0, 14].  The value alone,
-// u Phi(u), is rounded to bf16 as it stands, and a fit to 4.8e-6 is far below
-// half a step of that (2^-9).  The slope's two terms cancel near u = -0.75,
-// where that fit left 1.4e-3 of the result, so the backward takes three terms
-// more and 1.2e-8, a fifth of half an fp32 step: the same time there, while the
-// pack, nearer to its arithmetic, takes 82 us with them instead of 75.  One
-// reciprocal and one exp2 serve the value and the density, where erff and expf
-// took about twice the instructions.
-struct Gauss {
-  float cdf;      // Phi(u)
-  float bell;     // exp(-u^2 / 2)
-};
-template <int FINE>
-__device__ __forceinline__ float mills(float a) {
-  if constexpr (FINE) {
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.265f, a, 1.0f));
-    float q = 0.0308207776f;
-    q = __builtin_fmaf(q, t, -0.144228257f);
-    q = __builtin_fmaf(q, t, 0.217814239f);
-    q = __builtin_fmaf(q, t, -0.116361839f);
-    q = __builtin_fmaf(q, t, 0.137952611f);
-    q = __builtin_fmaf(q, t, 0.0603132998f);
-    q = __builtin_fmaf(q, t, 0.102700938f);
-    q = __builtin_fmaf(q, t, 0.10524667f);
-    q = __builtin_fmaf(q, t, 0.105741564f);
-    return q * t;
-  } else {
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31f, a, 1.0f));
-    float q = -0.0739293803f;
-    q = __builtin_fmaf(q, t, 0.180450903f);
-    q = __builtin_fmaf(q, t, 0.0157443031f);
-    q = __builtin_fmaf(q, t, 0.133429849f);
-    q = __builtin_fmaf(q, t, 0.12044131f);
-    q = __builtin_fmaf(q, t, 0.123860693f);
-    return q * t;
-  }
-}
-template <int FINE>
-__device__ __forceinline__ Gauss gauss(float u) {
-  const float ratio = mills<FINE>(fabsf(u));
-  const float bell = __builtin_amdgcn_exp2f(u * u * -0.72134752044f);
-  const float tail = ratio * bell;
-  return Gauss{u < 0.0f ? tail : 1.0f - tail, bell};
 }
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
