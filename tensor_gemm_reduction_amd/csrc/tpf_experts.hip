@@ -777,15 +777,24 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(CombineArgs args) {
     const int64_t t = u / per;
     const int c = (int)(u - t * per) * 8;
     float acc[8] = {};
-#pragma unroll 4
-    for (int j = 0; j < a.k; ++j) {
-      const int r = a.pos[t * a.k + j];
-      if ((uint32_t)r >= (uint64_t)R) continue;
-      const float w = a.weights[t * a.k + j];
-      float v[8];
-      load8<ROWS_F32>(a.rows, (int64_t)r * a.H + c, v);
+    for (int j0 = 0; j0 < a.k; j0 += 8) {       // the slots' rows first, then all their loads
+      int r[8];
+      float w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+      for (int j = 0; j < 8; ++j) {
+        const int64_t at = t * a.k + min(j0 + j, a.k - 1);
+        r[j] = j0 + j < a.k ? a.pos[at] : -1;
+        w[j] = a.weights[at];
+      }
+      float v[8][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((uint32_t)r[j] < (uint64_t)R) load8<ROWS_F32>(a.rows, (int64_t)r[j] * a.H + c, v[j]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((uint32_t)r[j] < (uint64_t)R)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[j], v[j][i], acc[i]);
     }
     store8<Y_F32>(a.y, t * a.H + c, acc);
   }
@@ -808,24 +817,33 @@ __global__ __launch_bounds__(256) void expert_combine_backward_kernel(CombineArg
     for (int c = threadIdx.x * 8; c < a.H; c += blockDim.x * 8) {
       float dy[8];
       load8<Y_F32>(a.dy, t * a.H + c, dy);
+      // Four slots' loads before their stores, which the compiler could not move them across.
 #pragma unroll
-      for (int j = 0; j < kExpertMaxK; ++j) {
-        if (j < a.k) {
-          const int r = a.pos[t * a.k + j];
-          if ((uint32_t)r < (uint64_t)R) {
-            const float w = a.weights[t * a.k + j];
-            float v[8], o[8];
-            load8<ROWS_F32>(a.rows, (int64_t)r * a.H + c, v);
+      for (int j0 = 0; j0 < kExpertMaxK; j0 += 4) {
+        if (j0 < a.k) {
+          int r[4];
+          float v[4][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              dot[j] = __builtin_fmaf(dy[i], v[i], dot[j]);
-              o[i] = w * dy[i];
-            }
-            store8<ROWS_F32>(a.drows, (int64_t)r * a.H + c, o);
+          for (int j = 0; j < 4; ++j) {
+            r[j] = j0 + j < a.k ? a.pos[t * a.k + j0 + j] : -1;
+            if ((uint32_t)r[j] < (uint64_t)R) load8<ROWS_F32>(a.rows, (int64_t)r[j] * a.H + c, v[j]);
           }
-          if (t * a.k + j >= used) {
-            const float zero[8] = {};
-            store8<ROWS_F32>(a.drows, (t * a.k + j) * a.H + c, zero);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if ((uint32_t)r[j] < (uint64_t)R) {
+              const float w = a.weights[t * a.k + j0 + j];
+              float o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                dot[j0 + j] = __builtin_fmaf(dy[i], v[j][i], dot[j0 + j]);
+                o[i] = w * dy[i];
+              }
+              store8<ROWS_F32>(a.drows, (int64_t)r[j] * a.H + c, o);
+            }
+            if (j0 + j < a.k && t * a.k + j0 + j >= used) {
+              const float zero[8] = {};
+              store8<ROWS_F32>(a.drows, (t * a.k + j0 + j) * a.H + c, zero);
+            }
           }
         }
       }

@@ -76,6 +76,7 @@ struct RowRange {
   int first, n;
 };
 __device__ __forceinline__ RowRange block_rows(const PackArgs& a, int blk, int lane) {
+  if ((int64_t)blk * kScaleBlock >= a.columns) return RowRange{0, 0};
   if (!a.offsets) return RowRange{blk * kScaleBlock, max(0, min(kScaleBlock, a.R - blk * kScaleBlock))};
   int before = 0;
   for (int base = 0; base < a.E; base += 64) {
@@ -104,90 +105,137 @@ __device__ __forceinline__ RowRange block_rows(const PackArgs& a, int blk, int l
   return RowRange{0, 0};
 }
 
-// A workgroup packs 512 columns of the transpose (four blocks of rows of u) of
-// 32 rows (columns of u): each block's 128 x 32 values go through LDS, turned.
-// The four blocks' scales of a row are one word, their codes 512 bytes.
-constexpr int kPackK = 32;
-__global__ __launch_bounds__(256) void scaled_pack_columns_kernel(PackArgs args) {
+// A workgroup packs a block of 128 rows x 128 columns of u down the columns, and
+// with ROWS along the rows as well, so that u is read once.  Thread (q, c) holds
+// rows 8 q .. 8 q + 7 of columns 8 c .. 8 c + 7: a row's largest value takes the
+// exchange of 16 lanes, a column's that of the wave's four q and the four waves.
+// The transpose's codes go through LDS, eight rows of a column at a time, their
+// places XORed with c so that 16 lanes write to all banks.
+// 4096 x 4096 both ways: rows and columns packed in passes of their own 26 us, in
+// one 22 (with two waves a SIMD, as the registers fall out by themselves, 31).  All
+// workgroups of that size run at once, so that loads and stores, 7 us each at
+// memory's rate, lie one behind the other; larger sizes overlap them.
+template <int ROWS>
+__global__ __launch_bounds__(256, 4) void scaled_pack_columns_kernel(PackArgs args) {
   (void)args;
   const PackArgs& a = *(const PackArgs*)__builtin_amdgcn_kernarg_segment_ptr();
-  __shared__ uint32_t codes[kPackK][129];     // 512 codes a row, one word of padding
-  __shared__ uint8_t exps[kPackK][4];
-  const int k = blockIdx.z, quad = blockIdx.x, c0 = blockIdx.y * kPackK;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 128];
+  __shared__ uint16_t tops[4][128];
+  const int k = blockIdx.z, blk = blockIdx.x, c0 = blockIdx.y * 128;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = threadIdx.x & 15, q = threadIdx.x >> 4;
   const uint16_t* u = reinterpret_cast<const uint16_t*>(a.u[k]);
-  // Wave w packs block w: lane l holds rows 2 (l / 4) + 32 i and the one after
-  // them, columns 8 (l % 4) .. + 7.
-  const int blk = quad * 4 + wave;
-  RowRange r{0, 0};
-  if (blk * kScaleBlock < a.columns) r = block_rows(a, blk, lane);
-  const int col = c0 + (lane & 3) * 8;
-  u32x4_t w[4][2];
+  const RowRange r = block_rows(a, blk, lane);
+  const int col = c0 + c * 8;
+  u32x4_t w[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 8; ++i) {
+    const int local = q * 8 + i;
+    w[i] = u32x4_t{0, 0, 0, 0};
+    if (local < r.n && col < a.K) {
+      int row = r.first + local;
+      if (a.src) row = a.src[row] / a.top;
+      if ((uint32_t)row < (uint32_t)a.M) w[i] = *reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.K + col);
+    }
+  }
+  const int xwidth = ((a.K + 127) / 128 + 3) >> 2 << 2, twidth = (a.columns / kScaleBlock + 3) >> 2 << 2;
+  if constexpr (ROWS) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int local = i * 32 + (lane >> 2) * 2 + h;
-      w[i][h] = u32x4_t{0, 0, 0, 0};
-      if (local < r.n && col < a.K) {
-        int row = r.first + local;
-        if (a.src) row = a.src[row] / a.top;
-        if ((uint32_t)row < (uint32_t)a.M) w[i][h] = *reinterpret_cast<const u32x4_t*>(u + (int64_t)row * a.K + col);
+    for (int i = 0; i < 8; ++i) {
+      uint32_t top = top_of(w[i]);
+#pragma unroll
+      for (int d = 1; d <= 8; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+      const int e = scale_byte(top);
+      const float inv = inverse(e);
+      if (q * 8 + i < r.n) {
+        const int64_t row = r.first + q * 8 + i;
+        if (col < a.K)
+          *reinterpret_cast<u32x2_t*>(a.codes[k] + row * a.K + col) =
+              u32x2_t{codes4(w[i][0], w[i][1], inv), codes4(w[i][2], w[i][3], inv)};
+        if (c == 0) a.scales[k][row * xwidth + blockIdx.y] = (uint8_t)e;
       }
     }
-  // Each of the lane's eight columns: the largest of its 8 rows, then over the 16 lanes of the column.
+  }
+  // The columns' largest values: of the thread's rows, the wave's, then all.
+  uint32_t even[4] = {}, odd[4] = {};
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    uint32_t top = 0;
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t v = (c & 1 ? w[i][h][c >> 1] >> 16 : w[i][h][c >> 1]) & 0x7fffu;
-        if (v < 0x7f80u) top = max(top, v);
-      }
-#pragma unroll
-    for (int d = 4; d <= 32; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    const int e = scale_byte(top);
-    const float inv = inverse(e);
-    const int kr = (lane & 3) * 8 + c;
-    if (lane < 4) exps[kr][wave] = (uint8_t)e;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b0 = c & 1 ? w[i][0][c >> 1] & 0xffff0000u : w[i][0][c >> 1] << 16;
-      const uint32_t b1 = c & 1 ? w[i][1][c >> 1] & 0xffff0000u : w[i][1][c >> 1] << 16;
-      const uint32_t two = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(scaled(b0, inv), scaled(b1, inv), 0, false);
-      reinterpret_cast<uint16_t*>(&codes[kr][wave * 32])[i * 16 + (lane >> 2)] = (uint16_t)two;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = w[i][j] & 0x7fffu, hi = (w[i][j] >> 16) & 0x7fffu;
+      if (lo < 0x7f80u) even[j] = max(even[j], lo);
+      if (hi < 0x7f80u) odd[j] = max(odd[j], hi);
     }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int d = 16; d <= 32; d <<= 1) {
+      even[j] = max(even[j], (uint32_t)__shfl_xor((int)even[j], d));
+      odd[j] = max(odd[j], (uint32_t)__shfl_xor((int)odd[j], d));
+    }
+    if (lane < 16) *reinterpret_cast<uint32_t*>(&tops[wave][c * 8 + 2 * j]) = even[j] | odd[j] << 16;
   }
   __syncthreads();
-  const int width = (a.columns / kScaleBlock + 3) >> 2;
-  for (int i = threadIdx.x; i < kPackK * 32; i += 256) {
-    const int kr = i >> 5, part = i & 31;               // 16 bytes each
-    const int x = quad * 512 + part * 16;
-    if (c0 + kr < a.K && x < a.columns) {
-      const uint32_t* from = &codes[kr][part * 4];
-      *reinterpret_cast<u32x4_t*>(a.codes_t[k] + (int64_t)(c0 + kr) * a.columns + x) =
-          u32x4_t{from[0], from[1], from[2], from[3]};
+  int e[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const uint32_t t = *reinterpret_cast<const uint32_t*>(&tops[v][c * 8 + 2 * j]);
+      lo = max(lo, t & 0xffffu);
+      hi = max(hi, t >> 16);
     }
+    e[2 * j] = scale_byte(lo);
+    e[2 * j + 1] = scale_byte(hi);
   }
-  if (threadIdx.x < kPackK && c0 + (int)threadIdx.x < a.K)
-    reinterpret_cast<uint32_t*>(a.scales_t[k])[(int64_t)(c0 + threadIdx.x) * width + quad] =
-        *reinterpret_cast<const uint32_t*>(exps[threadIdx.x]);
+  if (q == 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < a.K) a.scales_t[k][(int64_t)(col + j) * twidth + blk] = (uint8_t)e[j];
+  }
+  if (blk * kScaleBlock >= a.columns) return;            // a word's bytes behind the last block
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float inv = inverse(e[j]);
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = j & 1 ? w[i][j >> 1] & 0xffff0000u : w[i][j >> 1] << 16;
+    u32x2_t codes;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t t = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(scaled(v[4 * h], inv), scaled(v[4 * h + 1], inv), 0, false);
+      codes[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(scaled(v[4 * h + 2], inv), scaled(v[4 * h + 3], inv), (int)t, true);
+    }
+    *reinterpret_cast<u32x2_t*>(&turned[(c * 8 + j) * 128 + (q ^ c) * 8]) = codes;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = i * 256 + threadIdx.x, tc = at >> 3, part = at & 7;      // 16 rows of one column
+    if (c0 + tc >= a.K) continue;
+    const u32x2_t lo = *reinterpret_cast<const u32x2_t*>(&turned[tc * 128 + ((2 * part) ^ (tc >> 3)) * 8]);
+    const u32x2_t hi = *reinterpret_cast<const u32x2_t*>(&turned[tc * 128 + ((2 * part + 1) ^ (tc >> 3)) * 8]);
+    *reinterpret_cast<u32x4_t*>(a.codes_t[k] + (int64_t)(c0 + tc) * a.columns + blk * 128 + part * 16) =
+        u32x4_t{lo[0], lo[1], hi[0], hi[1]};
+  }
 }
 
 }  // namespace
 
 hipError_t launch_scaled_pack(const PackArgs& a, hipStream_t s) {
-  if (a.codes[0]) {
+  const bool together = a.codes[0] && a.codes_t[0] && !a.offsets;      // the columns' rows are the rows as they lie
+  if (a.codes[0] && !together) {
     const int64_t units = (int64_t)a.M * (scale_width(a.K) / 4);
-    hipLaunchKernelGGL(scaled_pack_rows_kernel, dim3((unsigned)std::min<int64_t>((units + 3) / 4, 1 << 22), a.p), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(scaled_pack_rows_kernel, dim3((unsigned)std::min<int64_t>((units + 3) / 4, 1 << 22), a.p), dim3(256),
+                       0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (a.codes_t[0]) {
-    const int quads = (a.columns / kScaleBlock + 3) / 4;
-    hipLaunchKernelGGL(scaled_pack_columns_kernel, dim3(quads, (a.K + kPackK - 1) / kPackK, a.p), dim3(256), 0, s, a);
+    // Words of scales end with the bytes of blocks that are not there: those too have a workgroup.
+    const dim3 grid((unsigned)scale_width(a.columns), (unsigned)(together ? scale_width(a.K) : scale_blocks(a.K)), a.p);
+    if (together) hipLaunchKernelGGL(scaled_pack_columns_kernel<1>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(scaled_pack_columns_kernel<0>, grid, dim3(256), 0, s, a);
     return hipGetLastError();
   }
   return hipSuccess;
