@@ -77,7 +77,7 @@ struct ScaledArgs {
 };
 // Tiles of 16 rows that the kernel for few rows takes for M rows (of E experts),
 // 0: the large tiles take them.
-int scaled_few_tiles(int64_t M, int64_t E);
+int scaled_few_tiles(int64_t M, int64_t N, int64_t blocks, int64_t E);
 hipError_t launch_scaled_few(const ScaledArgs& a, int wscale, int tiles, hipStream_t s);
 hipError_t launch_scaled_matmul(ScaledArgs a, int wscale, hipStream_t s);        // E > 0: experts' rows
 hipError_t launch_scaled_weight_grad(ScaledArgs a, hipStream_t s);               // E > 0: experts' gradients

@@ -10,6 +10,7 @@
 // conversions are small (192 cycles of a SIMD's 1260 that a block's 4 KB take at
 // 8 TB/s).
 #include <algorithm>
+#include <type_traits>
 
 #include "tpf_gemm.hpp"
 #include "tpf_scaled.hpp"
@@ -173,24 +174,39 @@ hipError_t launch_few_sized(const ScaledArgs& a, hipStream_t s) {
   return eight ? launch_few<TM, 2, 8, EXPERTS, WS>(a, s) : launch_few<TM, 2, 4, EXPERTS, WS>(a, s);
 }
 
-template <int EXPERTS, int WS>
-hipError_t launch_few_rows(const ScaledArgs& a, int tm, hipStream_t s) {
-  if (tm == 1) return launch_few_sized<1, EXPERTS, WS>(a, s);
-  if (tm == 2) return launch_few_sized<2, EXPERTS, WS>(a, s);
-  return launch_few_sized<4, EXPERTS, WS>(a, s);
-}
-
 }  // namespace
 
-int scaled_few_tiles(int64_t M, int64_t E) {
-  const int64_t rows = E ? (M + E - 1) / E : M;      // of an expert, if all get as many
-  if (E) return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 40 ? 4 : 0;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
+// Against the tiles, whose rows and columns of 128 leave compute units idle where
+// there are few of both (us, this kernel and the tiles; weights N x K, M rows):
+// with a workgroup a compute unit or fewer this kernel wins, of its forms the one
+// of fewest rows (4096 x 4096: M 1 9.9 and 20.4, M 32 10.2 and 20.1, M 64 13.4 and
+// 20.3, M 128 18.6 and 21.0, M 192 would be two rounds; 1024 x 8192, M 256: 21.7
+// and 36.6); with two, weights read again by each are most of the time (8192 x
+// 8192, M 96: 55 and 52; 16384 x 4096, M 48: 38 and 29), but for a form that reads
+// them once (16384 x 4096, M 32: 23 and 29).  Up to 16 rows read them once whatever
+// their width (28672 x 8192: 52 and 58 at M 1, 60 and 59 at M 16).
+//
+// Experts' workgroups are many, each of a stream as long as the contraction: with
+// 32 blocks or more this kernel wins up to 8 rows an expert (8 x 4096 x 4096, 4
+// each: 33 and 44; 64 x 1024 x 4096, 2 each: 55 and 57, 16 each: 86 and 67), with
+// fewer the tiles, if they fill the chip (64 x 4096 x 1024, 2 each: 73 and 58; 256
+// x 512 x 2048, 2 each: 69 and 51; but 32 x 512 x 2048, 4 each: 11.3 and 13.5).
+int scaled_few_tiles(int64_t M, int64_t N, int64_t blocks, int64_t E) {
+  const int64_t across = (N + 31) / 32;
+  if (E) return M <= 8 * E && (blocks >= 32 || E * across <= 512) ? 1 : 0;
+  const auto groups = [&](int tm) { return (M + 16 * tm - 1) / (16 * tm) * across; };
+  if (M <= 16 || groups(1) <= 256) return 1;
+  if (groups(2) <= (M <= 32 ? 512 : 256)) return 2;
+  return groups(4) <= 256 ? 4 : 0;
 }
 
 hipError_t launch_scaled_few(const ScaledArgs& a, int wscale, int tm, hipStream_t s) {
-  if (a.E) return wscale == WS_F32 ? launch_few_rows<1, WS_F32>(a, tm, s) : launch_few_rows<1, WS_BYTE>(a, tm, s);
-  return wscale == WS_F32 ? launch_few_rows<0, WS_F32>(a, tm, s) : launch_few_rows<0, WS_BYTE>(a, tm, s);
+  const auto go = [&](auto ws) {
+    constexpr int WS = decltype(ws)::value;
+    if (a.E) return launch_few_sized<1, 1, WS>(a, s);
+    return tm == 1 ? launch_few_sized<1, 0, WS>(a, s) : tm == 2 ? launch_few_sized<2, 0, WS>(a, s) : launch_few_sized<4, 0, WS>(a, s);
+  };
+  return wscale == WS_F32 ? go(std::integral_constant<int, WS_F32>()) : go(std::integral_constant<int, WS_BYTE>());
 }
 
 }  // namespace tpf

@@ -249,11 +249,22 @@ struct ScScales {
   }
 };
 
-// Row `row` of a slot: the lane's 32 codes.
-__device__ __forceinline__ i32x8_t sc_read(const char* l, int row, int lane) {
-  const int g = lane >> 4, z = sc_swz(row);
-  const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(l + row * 128 + 16 * (g ^ z));
-  const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(l + row * 128 + 16 * ((g + 4) ^ z));
+// Where the lane's 32 codes of a wave's first 16 rows lie in a slot: rows 16
+// further on are 2 KiB further on, their swizzle being the same.  One offset and a
+// constant a read: through longer chains of address arithmetic the compiler loses
+// which slot a read is of, and then waits for every load in flight.
+struct ScPlace {
+  int lo, hi;
+  __device__ __forceinline__ ScPlace(int row0, int lane) {
+    const int row = row0 + (lane & 15), g = lane >> 4, z = sc_swz(row);
+    lo = row * 128 + 16 * (g ^ z);
+    hi = row * 128 + 16 * ((g + 4) ^ z);
+    asm volatile("" : "+v"(lo), "+v"(hi));
+  }
+};
+__device__ __forceinline__ i32x8_t sc_read(const char* slot, const ScPlace& at, int rows) {
+  const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(slot + (at.lo + rows * 128));
+  const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(slot + (at.hi + rows * 128));
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -281,12 +292,11 @@ __device__ __forceinline__ void sc_take(ScFine& to, i32x8_t v) { to = sc_fine(v)
 // that this step's w was read from a step ago.
 template <class Cfg, int MODE, int WS, int FINE, int T>
 __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOperands<Cfg, FINE>& o,
-                                        ScLoader<Cfg, MODE>& ld, ScScales<Cfg, MODE, WS>& sc, const ScaledArgs& a, int kbs) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r16 = lane & 15;
-  const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
+                                        ScLoader<Cfg, MODE>& ld, ScScales<Cfg, MODE, WS>& sc, const ScPlace& px,
+                                        const ScPlace& pw, const ScaledArgs& a, int kbs) {
+  const int lane = threadIdx.x & 63;
   constexpr int SX = T % 3, SW = T % 2, S = Cfg::SLICES;
   constexpr int XL = Cfg::X_LOADS, PER = (XL + S - 2) / (S - 1);
-  const char* lx = x_slot<Cfg, SX>();
   sc.load();
   float wf[WS == WS_ROW && FINE ? Cfg::TN : 1][4];
   if constexpr (FINE && WS == WS_ROW) {
@@ -302,13 +312,12 @@ __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOper
   for (int s = 0; s < S; ++s) {
     if (s < S - 1) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) o.x[(s + 1) & 1][i] = sc_read(lx, wm * Cfg::WM + (2 * s + 2 + i) * 16 + r16, lane);
+      for (int i = 0; i < 2; ++i) o.x[(s + 1) & 1][i] = sc_read(x_slot<Cfg, SX>(), px, (2 * s + 2 + i) * 16);
     } else {
       wait_vmcnt(XL);
       lds_barrier();
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        o.x[0][i] = sc_read(x_slot<Cfg, (SX + 1) % 3>(), wm * Cfg::WM + i * 16 + r16, lane);
+      for (int i = 0; i < 2; ++i) o.x[0][i] = sc_read(x_slot<Cfg, (SX + 1) % 3>(), px, i * 16);
     }
     ScFine xf[2];
     if constexpr (FINE) {
@@ -341,7 +350,7 @@ __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOper
         for (int q = 0; q < XL; ++q)      // slice s issues loads PER s .. PER (s + 1) - 1, spread over its columns
           if (q / PER == s && (q % PER) * Cfg::TN / PER == n) ld.x_load(q, a.K, x_slot<Cfg, (SX + 2) % 3>());
       } else {
-        sc_take(o.w[n], sc_read(w_slot<Cfg, (SW + 1) % 2>(), wn * Cfg::WN + n * 16 + r16, lane));
+        sc_take(o.w[n], sc_read(w_slot<Cfg, (SW + 1) % 2>(), pw, n * 16));
 #pragma unroll
         for (int q = 0; q < Cfg::W_LOADS; ++q)
           if (q * Cfg::TN / Cfg::W_LOADS == n) ld.w_load(q, a.K, w_slot<Cfg, SW>());
@@ -359,18 +368,18 @@ __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOper
 
 template <class Cfg, int MODE, int WS, int FINE, int T>
 __device__ __forceinline__ void sc_steps(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOperands<Cfg, FINE>& o,
-                                         ScLoader<Cfg, MODE>& ld, ScScales<Cfg, MODE, WS>& sc, const ScaledArgs& a,
-                                         const ScJob& j, int t) {
+                                         ScLoader<Cfg, MODE>& ld, ScScales<Cfg, MODE, WS>& sc, const ScPlace& px,
+                                         const ScPlace& pw, const ScaledArgs& a, const ScJob& j, int t) {
   if constexpr (T < 6) {
     if (t + T < j.steps) {
-      sc_step<Cfg, MODE, WS, FINE, T>(acc, o, ld, sc, a, j.kbs);
-      sc_steps<Cfg, MODE, WS, FINE, T + 1>(acc, o, ld, sc, a, j, t);
+      sc_step<Cfg, MODE, WS, FINE, T>(acc, o, ld, sc, px, pw, a, j.kbs);
+      sc_steps<Cfg, MODE, WS, FINE, T + 1>(acc, o, ld, sc, px, pw, a, j, t);
     }
   }
 }
 
-template <class Cfg, int MODE, int WS, int OUT, int ACT>
-__global__ __launch_bounds__(Cfg::THREADS) void scaled_tile_kernel(ScaledArgs args) {
+template <class Cfg, int MODE, int WS, int OUT>
+__global__ __launch_bounds__(Cfg::THREADS, 2) void scaled_tile_kernel(ScaledArgs args) {
   (void)args;
   const ScaledArgs& a = *(const ScaledArgs*)__builtin_amdgcn_kernarg_segment_ptr();
   constexpr int FINE = OUT == OUT_F32;
@@ -451,11 +460,12 @@ __global__ __launch_bounds__(Cfg::THREADS) void scaled_tile_kernel(ScaledArgs ar
     wait_vmcnt(Cfg::X_LOADS + Cfg::W_LOADS);
     lds_barrier();
     ScOperands<Cfg, FINE> o;
+    const ScPlace px(wm * Cfg::WM, lane), pw(wn * Cfg::WN, lane);
 #pragma unroll
-    for (int n = 0; n < Cfg::TN; ++n) sc_take(o.w[n], sc_read(w_slot<Cfg, 0>(), wn * Cfg::WN + n * 16 + r16, lane));
+    for (int n = 0; n < Cfg::TN; ++n) sc_take(o.w[n], sc_read(w_slot<Cfg, 0>(), pw, n * 16));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) o.x[0][i] = sc_read(x_slot<Cfg, 0>(), wm * Cfg::WM + i * 16 + r16, lane);
-    for (int t = 0; t < j.steps; t += 6) sc_steps<Cfg, MODE, WS, FINE, 0>(acc, o, ld, sc, a, j, t);
+    for (int i = 0; i < 2; ++i) o.x[0][i] = sc_read(x_slot<Cfg, 0>(), px, i * 16);
+    for (int t = 0; t < j.steps; t += 6) sc_steps<Cfg, MODE, WS, FINE, 0>(acc, o, ld, sc, px, pw, a, j, t);
     wait_vmcnt(0);                                 // the repeated loads past the last step
   }
 
@@ -469,7 +479,7 @@ __global__ __launch_bounds__(Cfg::THREADS) void scaled_tile_kernel(ScaledArgs ar
 #pragma unroll
     for (int n = 0; n < Cfg::TN; n += 2) {
       f32x4_t v[2] = {acc[m][n], acc[m][n + 1]};
-      if constexpr (ACT) v[0] = sc_gelu(v[0]), v[1] = sc_gelu(v[1]);
+      if ((MODE == PLAIN || MODE == EXPERTS) && a.gelu) v[0] = sc_gelu(v[0]), v[1] = sc_gelu(v[1]);
       const int col0 = wn * Cfg::WN + n * 16;
       if constexpr (OUT == OUT_F32) {
 #pragma unroll
@@ -503,29 +513,36 @@ hipError_t launch_cfg(ScaledArgs a, hipStream_t s) {
   if (MODE == GRAD || MODE == EXPERTS_GRAD) tasks *= a.p * (MODE == EXPERTS_GRAD ? a.E : 1);
   if (tasks > 1 << 23) return hipErrorInvalidConfiguration;
   a.tasks = (int)tasks;
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(a.tasks), dim3(Cfg::THREADS), 0, s, a); };
-  if constexpr (MODE == PLAIN || MODE == EXPERTS) {
-    // GeLU in instances of its own: skipped in the others' code, its 128 inlined copies cost most of a short tile's
-    // time in instruction fetches (32768 rows of 64 experts, K 1024, N 4096: 306 us, without them TIME).
-    a.gelu ? go(scaled_tile_kernel<Cfg, MODE, WS, OUT, 1>) : go(scaled_tile_kernel<Cfg, MODE, WS, OUT, 0>);
-  } else {
-    go(scaled_tile_kernel<Cfg, MODE, WS, OUT, 0>);
-  }
+  hipLaunchKernelGGL((scaled_tile_kernel<Cfg, MODE, WS, OUT>), dim3(a.tasks), dim3(Cfg::THREADS), 0, s, a);
   return hipGetLastError();
 }
 
+// Tiles of 256 x 256 take half the LDS reads of four of 128 x 128 and are 30 %
+// faster where they fill the compute units, one on each; those of 128, two on each,
+// leave fewer idle.  A round of 256 of the large takes as long as 750 of the small
+// and what their start and end costs, 110 more (4096 rows and columns, K 4096: 60
+// us and 77; 2560 x 4096: 53 and 58; 2048 x 4096: 53 and 42; 4352 x 4096, two
+// rounds: 98 and 88).  An expert's last tile is half full (64 x 4096 x 2048, rows
+// an expert: 96: 150 and 135, 192: 161 and 192).  The large have no registers for
+// partial sums: bf16 results and scales of powers of two only.
 template <int MODE, int WS>
 hipError_t launch_mode(const ScaledArgs& a, int64_t rows, int64_t outs, hipStream_t s) {
-  const int64_t big = (rows + 255) / 256 * ((a.N + 255) / 256) * outs;
   if (a.out == OUT_F32) return launch_cfg<Mid, MODE, WS, OUT_F32>(a, s);
-  if constexpr (WS == WS_F32) return launch_cfg<Mid, MODE, WS, OUT_BF16>(a, s);
-  else return big >= 192 ? launch_cfg<Big, MODE, WS, OUT_BF16>(a, s) : launch_cfg<Mid, MODE, WS, OUT_BF16>(a, s);
+  if constexpr (WS != WS_F32) {
+    const auto tiles = [&](int64_t b) {
+      const int64_t down = MODE == EXPERTS ? rows / b + a.E / 2 : (rows + b - 1) / b;
+      return down * ((a.N + b - 1) / b) * outs;
+    };
+    const int64_t rounds = (tiles(256) + 255) / 256;
+    if (750 * rounds <= tiles(128) + 110) return launch_cfg<Big, MODE, WS, OUT_BF16>(a, s);
+  }
+  return launch_cfg<Mid, MODE, WS, OUT_BF16>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_scaled_matmul(ScaledArgs a, int wscale, hipStream_t s) {
-  if (const int few = scaled_few_tiles(a.M, a.E)) return launch_scaled_few(a, wscale, few, s);
+  if (const int few = scaled_few_tiles(a.M, a.N, a.p * scale_blocks(a.K), a.E)) return launch_scaled_few(a, wscale, few, s);
   if (a.E) {
     return wscale == WS_F32 ? launch_mode<EXPERTS, WS_F32>(a, a.M, 1, s) : launch_mode<EXPERTS, WS_BYTE>(a, a.M, 1, s);
   }
