@@ -413,12 +413,12 @@ size_t tpf_qweight_matmul_ws(int p, int64_t M, int64_t K, int64_t N, int group);
  * 128 along the contraction; sums are fp32.  Conventions as above.
  *
  * A packed operand [M, K] is codes [M, K] and scales [M, S], S = ceil(K / 128)
- * rounded up to a multiple of 4: byte e of block b stands for 2^(e-127), so row m
- * holds code[m][j] 2^(scales[m][j / 128] - 127).  K is a multiple of 16.
+ * rounded up to a multiple of 4: byte e of block b stands for 2^(e-127) (255: NaN),
+ * so row m holds code[m][j] 2^(scales[m][j / 128] - 127).  K is a multiple of 16.
  * ------------------------------------------------------------------------- */
 
 /* Scales of a weight's blocks of 128 x 128. */
-#define TPF_SCALE_BYTE 0         /* bytes, 2^(e-127) */
+#define TPF_SCALE_BYTE 0         /* bytes, 2^(e-127), 255: NaN */
 #define TPF_SCALE_F32 1          /* fp32 factors */
 
 /* Packs u[k] [M, K] bf16: scales hold the least power of two, not below 2^-117,
@@ -483,7 +483,8 @@ int tpf_scaled_weight_grad(tpf_handle h, int p, int64_t Mt, int64_t R, int64_t C
  *   offsets: [E + 1], expert e's rows are offsets[e] .. offsets[e+1] - 1.
  *   src: [T k], the slot of each row, -1 behind the last row.
  *   pos: [T, k], the row of each slot, -1 for tokens that are not routed.
- * All results are int32 but for weights.  k <= E / groups * top_groups. */
+ * All results are int32 but for weights.  k <= E / groups * top_groups, T k fits in
+ * 31 bits, T <= 2^31 - 1 - 2^17. */
 int tpf_expert_route(tpf_handle h, int64_t T, int64_t E, int k, const void* logits, int dtype, int score,
                      const float* bias, int groups, int top_groups, int renorm, double scale, const uint8_t* mask,
                      int32_t* ids, float* weights, int32_t* offsets, int32_t* src, int32_t* pos, void* ws,

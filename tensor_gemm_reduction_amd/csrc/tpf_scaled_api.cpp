@@ -89,7 +89,8 @@ int check_route(int64_t T, int64_t E, int k, int dtype, int score, double scale)
   if ((st = check_experts(E))) return st;
   if (k < 1 || k > kExpertMaxK || k > E)
     return fail(TPF_ERR_SHAPE, "k must be 1 to " + std::to_string(kExpertMaxK) + " and at most E");
-  if (T * k > INT32_MAX) return fail(TPF_ERR_SHAPE, "T k must fit in 31 bits");
+  // parts of the tokens are counted in 32 bits up to the end of the last one
+  if (T > INT32_MAX - (1 << 17) || T * k > INT32_MAX) return fail(TPF_ERR_SHAPE, "T k must fit in 31 bits, T within 2^31 - 2^17");
   if (!valid_dtype(dtype)) return fail(TPF_ERR_INVALID_ARG, "unknown dtype");
   if (score != TPF_SCORE_SOFTMAX && score != TPF_SCORE_SIGMOID) return fail(TPF_ERR_INVALID_ARG, "unknown score");
   if (!std::isfinite(scale) || scale == 0.0) return fail(TPF_ERR_INVALID_ARG, "scale must be finite and not 0");

@@ -46,8 +46,10 @@ __device__ __forceinline__ f32x4_t sc_mfma_fine(const ScFine& w, const ScFine& x
 __device__ __forceinline__ f32x4_t sc_gelu(f32x4_t v) {
   return f32x4_t{v[0] * gauss<1>(v[0]).cdf, v[1] * gauss<1>(v[1]).cdf, v[2] * gauss<1>(v[2]).cdf, v[3] * gauss<1>(v[3]).cdf};
 }
-// 2^(e - 127)
-__device__ __forceinline__ float exp_byte(int e) { return e == 0 ? 0x1p-127f : __uint_as_float((uint32_t)e << 23); }
+// 2^(e - 127), NaN for 255 as the matrix instruction takes it
+__device__ __forceinline__ float exp_byte(int e) {
+  return __uint_as_float((uint32_t)e << 23 | (e == 0 || e == 255 ? 0x400000u : 0u));
+}
 
 // Number `t` of the tiles of BM rows that the experts' rows are cut into, each
 // expert's from its first row on: the expert, the tile's first row and its
@@ -75,7 +77,7 @@ __device__ __forceinline__ RowTile expert_tile(const int* offsets, int E, int R,
     const uint64_t past = __ballot(before + upto > t);
     if (past) {
       const int at = __builtin_ctzll(past);
-      const int skip = t - (before + __builtin_amdgcn_readlane(upto - tiles, at));
+      const int skip = max(t - (before + __builtin_amdgcn_readlane(upto - tiles, at)), 0);
       const int first = __builtin_amdgcn_readlane(lo, at) + skip * BM;
       return RowTile{base + at, first, min(BM, __builtin_amdgcn_readlane(hi, at) - first)};
     }

@@ -511,7 +511,7 @@ hipError_t launch_cfg(ScaledArgs a, hipStream_t s) {
   if (MODE == EXPERTS) a.tiles_m = (expert_tiles(a.M, a.E, Cfg::BM) + 2 * kXcds - 1) / (2 * kXcds) * (2 * kXcds);
   int64_t tasks = (int64_t)a.tiles_m * a.tiles_n;
   if (MODE == GRAD || MODE == EXPERTS_GRAD) tasks *= a.p * (MODE == EXPERTS_GRAD ? a.E : 1);
-  if (tasks > 1 << 23) return hipErrorInvalidConfiguration;
+  if (tasks * Cfg::THREADS >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   a.tasks = (int)tasks;
   hipLaunchKernelGGL((scaled_tile_kernel<Cfg, MODE, WS, OUT>), dim3(a.tasks), dim3(Cfg::THREADS), 0, s, a);
   return hipGetLastError();

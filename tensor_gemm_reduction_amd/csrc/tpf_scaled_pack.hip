@@ -96,7 +96,7 @@ __device__ __forceinline__ RowRange block_rows(const PackArgs& a, int blk, int l
     const uint64_t past = __ballot(before + upto > blk);
     if (past) {
       const int at = __builtin_ctzll(past);
-      const int skip = blk - (before + __shfl(upto - blocks, at));
+      const int skip = max(blk - (before + __shfl(upto - blocks, at)), 0);
       const int f = __shfl(lo, at) + skip * kScaleBlock;
       return RowRange{f, min(kScaleBlock, __shfl(hi, at) - f)};
     }

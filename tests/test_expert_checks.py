@@ -174,3 +174,9 @@ def test_oracle_gradient_against_differences(score, renorm):
         slope = ((O.route_weights(up, ids, score, renorm, 1.7) - O.route_weights(down, ids, score, renorm, 1.7)) * dw).sum(1) / (2 * h)
         # the third derivative is below 10 |dw|: h^2 of it and 2^-52 / h of the quotient's rounding
         assert (slope - d[:, e]).abs().max() <= 10 * dw.abs().sum(1).max() * h * h + 2.0 ** -28
+
+
+def test_tokens_are_counted_in_32_bits_to_the_end_of_the_last_part():
+    for T, want in ((2 ** 31 - 1, SHAPE), (2 ** 31 - 2 ** 17, SHAPE), (2 ** 31 - 2 ** 17 - 1, INVALID)):     # the handle
+        assert route(T=T, E=1, k=1, nb=1 << 40) == want
+        assert rgrad(T=T, E=1, k=1) == want
