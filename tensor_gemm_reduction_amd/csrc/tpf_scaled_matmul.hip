@@ -30,9 +30,11 @@ namespace {
 
 enum Mode : int { PLAIN = 0, GRAD = 1, EXPERTS = 2, EXPERTS_GRAD = 3 };
 
-// BM x BN results a workgroup of WAVES_M x WAVES_N waves, one block of 128 a step.
-template <int BM_, int BN_, int WAVES_M_, int WAVES_N_>
+// BM x BN results a workgroup of WAVES_M x WAVES_N waves, one block of 128 a step;
+// W_SLOTS tiles of w in LDS.
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, int W_SLOTS_>
 struct ScCfg {
+  static constexpr int W_SLOTS = W_SLOTS_, UNROLL = W_SLOTS == 1 ? 3 : 6;      // steps until the slots' turn is over
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
   static constexpr int NW = WAVES_M * WAVES_N, THREADS = 64 * NW;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, TM = WM / 16, TN = WN / 16;
@@ -43,7 +45,7 @@ struct ScCfg {
   static_assert(SLICES % 2 == 0, "slices alternate between two sets of registers");
 };
 
-// Three slots of x's tiles and two of w's, each an object of its own, so that the
+// Three slots of x's tiles and one or two of w's, each an object of its own, so that the
 // compiler sees that loads in flight into one do not touch what is read.
 template <class Cfg, int S>
 __device__ __forceinline__ char* x_slot() {
@@ -290,13 +292,18 @@ __device__ __forceinline__ void sc_take(ScFine& to, i32x8_t v) { to = sc_fine(v)
 // passes a barrier; between the last slice's instructions it reads the next step's
 // w, column by column, and loads the tile of w for the step after into the slot
 // that this step's w was read from a step ago.
+// With one slot of w (two workgroups then share a compute unit) a barrier at the
+// step's start says that all waves hold w; the next step's tile replaces it during
+// the first slice, x's loads follow in the second.
 template <class Cfg, int MODE, int WS, int FINE, int T>
 __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOperands<Cfg, FINE>& o,
                                         ScLoader<Cfg, MODE>& ld, ScScales<Cfg, MODE, WS>& sc, const ScPlace& px,
                                         const ScPlace& pw, const ScaledArgs& a, int kbs) {
   const int lane = threadIdx.x & 63;
-  constexpr int SX = T % 3, SW = T % 2, S = Cfg::SLICES;
+  constexpr int SX = T % 3, SW = T % Cfg::W_SLOTS, S = Cfg::SLICES;
   constexpr int XL = Cfg::X_LOADS, PER = (XL + S - 2) / (S - 1);
+  constexpr bool ONE = Cfg::W_SLOTS == 1;
+  if constexpr (ONE) lds_barrier();
   sc.load();
   float wf[WS == WS_ROW && FINE ? Cfg::TN : 1][4];
   if constexpr (FINE && WS == WS_ROW) {
@@ -307,9 +314,10 @@ __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOper
   } else if constexpr (FINE) {
     wf[0][0] = WS == WS_F32 ? sc.f : exp_byte(sc.w_byte);
   }
-  ld.next(a, kbs);
+  if constexpr (!ONE) ld.next(a, kbs);
 #pragma unroll
   for (int s = 0; s < S; ++s) {
+    if (ONE && s == 1) ld.next(a, kbs);
     if (s < S - 1) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) o.x[(s + 1) & 1][i] = sc_read(x_slot<Cfg, SX>(), px, (2 * s + 2 + i) * 16);
@@ -348,12 +356,20 @@ __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOper
       if (s < S - 1) {
 #pragma unroll
         for (int q = 0; q < XL; ++q)      // slice s issues loads PER s .. PER (s + 1) - 1, spread over its columns
-          if (q / PER == s && (q % PER) * Cfg::TN / PER == n) ld.x_load(q, a.K, x_slot<Cfg, (SX + 2) % 3>());
-      } else {
-        sc_take(o.w[n], sc_read(w_slot<Cfg, (SW + 1) % 2>(), pw, n * 16));
+          if (ONE ? s == 1 && q * Cfg::TN / XL == n : q / PER == s && (q % PER) * Cfg::TN / PER == n)
+            ld.x_load(q, a.K, x_slot<Cfg, (SX + 2) % 3>());
+        if constexpr (ONE) {
 #pragma unroll
-        for (int q = 0; q < Cfg::W_LOADS; ++q)
-          if (q * Cfg::TN / Cfg::W_LOADS == n) ld.w_load(q, a.K, w_slot<Cfg, SW>());
+          for (int q = 0; q < Cfg::W_LOADS; ++q)
+            if (s == 0 && q * Cfg::TN / Cfg::W_LOADS == n) ld.w_load(q, a.K, w_slot<Cfg, 0>());
+        }
+      } else {
+        sc_take(o.w[n], sc_read(w_slot<Cfg, (SW + 1) % Cfg::W_SLOTS>(), pw, n * 16));
+        if constexpr (!ONE) {
+#pragma unroll
+          for (int q = 0; q < Cfg::W_LOADS; ++q)
+            if (q * Cfg::TN / Cfg::W_LOADS == n) ld.w_load(q, a.K, w_slot<Cfg, SW>());
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);     // reads of later slices would need more registers than there are
@@ -370,7 +386,7 @@ template <class Cfg, int MODE, int WS, int FINE, int T>
 __device__ __forceinline__ void sc_steps(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOperands<Cfg, FINE>& o,
                                          ScLoader<Cfg, MODE>& ld, ScScales<Cfg, MODE, WS>& sc, const ScPlace& px,
                                          const ScPlace& pw, const ScaledArgs& a, const ScJob& j, int t) {
-  if constexpr (T < 6) {
+  if constexpr (T < Cfg::UNROLL) {
     if (t + T < j.steps) {
       sc_step<Cfg, MODE, WS, FINE, T>(acc, o, ld, sc, px, pw, a, j.kbs);
       sc_steps<Cfg, MODE, WS, FINE, T + 1>(acc, o, ld, sc, px, pw, a, j, t);
@@ -454,10 +470,12 @@ __global__ __launch_bounds__(Cfg::THREADS, 2) void scaled_tile_kernel(ScaledArgs
     ld.next(a, j.kbs);
 #pragma unroll
     for (int q = 0; q < Cfg::X_LOADS; ++q) ld.x_load(q, a.K, x_slot<Cfg, 1>());
+    if constexpr (Cfg::W_SLOTS == 2) {
 #pragma unroll
-    for (int q = 0; q < Cfg::W_LOADS; ++q) ld.w_load(q, a.K, w_slot<Cfg, 1>());
+      for (int q = 0; q < Cfg::W_LOADS; ++q) ld.w_load(q, a.K, w_slot<Cfg, 1>());
+    }
     sc.init(a, j);                                 // behind the tiles' loads: one latency covers both
-    wait_vmcnt(Cfg::X_LOADS + Cfg::W_LOADS);
+    wait_vmcnt(Cfg::X_LOADS + (Cfg::W_SLOTS == 2 ? Cfg::W_LOADS : 0));
     lds_barrier();
     ScOperands<Cfg, FINE> o;
     const ScPlace px(wm * Cfg::WM, lane), pw(wn * Cfg::WN, lane);
@@ -465,7 +483,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 2) void scaled_tile_kernel(ScaledArgs
     for (int n = 0; n < Cfg::TN; ++n) sc_take(o.w[n], sc_read(w_slot<Cfg, 0>(), pw, n * 16));
 #pragma unroll
     for (int i = 0; i < 2; ++i) o.x[0][i] = sc_read(x_slot<Cfg, 0>(), px, i * 16);
-    for (int t = 0; t < j.steps; t += 6) sc_steps<Cfg, MODE, WS, FINE, 0>(acc, o, ld, sc, px, pw, a, j, t);
+    for (int t = 0; t < j.steps; t += Cfg::UNROLL) sc_steps<Cfg, MODE, WS, FINE, 0>(acc, o, ld, sc, px, pw, a, j, t);
     wait_vmcnt(0);                                 // the repeated loads past the last step
   }
 
@@ -501,8 +519,9 @@ __global__ __launch_bounds__(Cfg::THREADS, 2) void scaled_tile_kernel(ScaledArgs
   }
 }
 
-using Big = ScCfg<256, 256, 2, 4>;
-using Mid = ScCfg<128, 128, 2, 2>;
+using Big = ScCfg<256, 256, 2, 4, 2>;
+using Tall = ScCfg<128, 256, 1, 4, 1>;
+using Mid = ScCfg<128, 128, 2, 2, 2>;
 
 template <class Cfg, int MODE, int WS, int OUT>
 hipError_t launch_cfg(ScaledArgs a, hipStream_t s) {
@@ -517,24 +536,39 @@ hipError_t launch_cfg(ScaledArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Tiles of 256 x 256 take half the LDS reads of four of 128 x 128 and are 30 %
-// faster where they fill the compute units, one on each; those of 128, two on each,
-// leave fewer idle.  A round of 256 of the large takes as long as 750 of the small
-// and what their start and end costs, 110 more (4096 rows and columns, K 4096: 60
-// us and 77; 2560 x 4096: 53 and 58; 2048 x 4096: 53 and 42; 4352 x 4096, two
-// rounds: 98 and 88).  An expert's last tile is half full (64 x 4096 x 2048, rows
-// an expert: 96: 150 and 135, 192: 161 and 192).  The large have no registers for
-// partial sums: bf16 results and scales of powers of two only.
+// Which tiles, by what their rounds over the compute units cost, in times of a
+// 128 x 128 tile when they fill the chip:
+//   256 x 256, one a compute unit, 750 a round of 256: half the LDS reads of four
+//     small ones, 30 % faster where they fill the rounds;
+//   128 x 256, two a compute unit, for experts, 825 a round of 512: as few LDS
+//     reads but half as many rows lost at an expert's end, and a tile's start and
+//     end beside the other's steps (so 700 where an expert's gradient sums up to
+//     1024 rows), against half again the loads;
+//   128 x 128, two a compute unit: 1 each and 110 for the start and the end.
+// An expert's last tile counts as half full.  Measured, us, in this order: 4096 x
+// 4096 x 4096: 60, 69, 77; 2560 x 4096: 53, 58, 58; 2048 x 4096: 52, 46, 42; 4352 x
+// 4096, two rounds: 97, 88, 89.  64 experts of K 1024, N 4096, rows drawn evenly,
+// 128 each: 103, 96, 107, 512: 219, 209, 257, drawn with a power of -0.7: 226, 207,
+// 251; 16 experts of K and N 4096, 512: 170, 190, 194.  Gradients 16 x 4096 x 1024,
+// rows an expert 512: 74, 69, 81, 4096: 283, 292, 352.
+// The first two have no registers for partial sums: bf16 results and scales of
+// powers of two only.
 template <int MODE, int WS>
 hipError_t launch_mode(const ScaledArgs& a, int64_t rows, int64_t outs, hipStream_t s) {
   if (a.out == OUT_F32) return launch_cfg<Mid, MODE, WS, OUT_F32>(a, s);
   if constexpr (WS != WS_F32) {
-    const auto tiles = [&](int64_t b) {
-      const int64_t down = MODE == EXPERTS ? rows / b + a.E / 2 : (rows + b - 1) / b;
-      return down * ((a.N + b - 1) / b) * outs;
+    constexpr bool TALL = MODE == EXPERTS || MODE == EXPERTS_GRAD;
+    const auto tiles = [&](int64_t bm, int64_t bn) {
+      const int64_t down = MODE == EXPERTS ? rows / bm + a.E / 2 : (rows + bm - 1) / bm;
+      return down * ((a.N + bn - 1) / bn) * outs;
     };
-    const int64_t rounds = (tiles(256) + 255) / 256;
-    if (750 * rounds <= tiles(128) + 110) return launch_cfg<Big, MODE, WS, OUT_BF16>(a, s);
+    const int64_t big = (tiles(256, 256) + 255) / 256 * 750, mid = tiles(128, 128) + 110;
+    if constexpr (TALL) {
+      const bool brief = MODE == EXPERTS_GRAD && a.K <= (int64_t)1024 * a.E;
+      const int64_t tall = (tiles(128, 256) + 511) / 512 * (brief ? 700 : 825);
+      if (tall < big && tall <= mid) return launch_cfg<Tall, MODE, WS, OUT_BF16>(a, s);
+    }
+    if (big <= mid) return launch_cfg<Big, MODE, WS, OUT_BF16>(a, s);
   }
   return launch_cfg<Mid, MODE, WS, OUT_BF16>(a, s);
 }

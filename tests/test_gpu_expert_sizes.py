@@ -35,8 +35,8 @@ def test_matmul_of_many_rows_with_gelu_on_large_tiles():
     check_sum(y, xv @ wv.t(), xv.abs() @ wv.abs().t(), K, BF, True)
 
 
-# (T, E, k, K, N): tiles of 128 and of 256, rows of no expert
-@pytest.mark.parametrize("T,E,k,K,N", [(4000, 3, 2, 144, 1032), (8000, 3, 2, 272, 1016), (3000, 60, 4, 144, 1032)])
+# (T, E, k, K, N): tiles of 128 x 128, 256 x 256 and 128 x 256, rows of no expert
+@pytest.mark.parametrize("T,E,k,K,N", [(4000, 3, 2, 144, 1032), (8000, 3, 2, 272, 1016), (3000, 60, 4, 144, 1032), (4000, 60, 4, 144, 2056)])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("act", [False, True])
 def test_expert_matmul_of_many_rows(T, E, k, K, N, gather, act):
@@ -60,7 +60,7 @@ def test_expert_matmul_of_many_rows(T, E, k, K, N, gather, act):
     assert (y[int(r.offsets[-1]):] == 0).all()
 
 
-@pytest.mark.parametrize("T,E,k,R,C,p", [(1500, 16, 2, 1000, 1032, 1), (900, 5, 2, 776, 520, 4)])
+@pytest.mark.parametrize("T,E,k,R,C,p", [(1500, 16, 2, 1000, 1032, 1), (900, 5, 2, 776, 520, 4), (2500, 2, 1, 2048, 2048, 2)])
 def test_expert_weight_grad_of_large_tiles(T, E, k, R, C, p):
     g = gen("bigdw", T, E)
     r = route_of(g, T, E, k, 1.0, True)
