@@ -48,7 +48,7 @@ __device__ __forceinline__ f32x4_t sc_gelu(f32x4_t v) {
 }
 // 2^(e - 127), NaN for 255 as the matrix instruction takes it
 __device__ __forceinline__ float exp_byte(int e) {
-  return __uint_as_float((uint32_t)e << 23 | (e == 0 || e == 255 ? 0x400000u : 0u));
+  return __uint_as_float((uint32_t)e << 23 | ((uint32_t)e - 1u >= 254u ? 0x400000u : 0u));
 }
 
 // Number `t` of the tiles of BM rows that the experts' rows are cut into, each

@@ -308,9 +308,11 @@ __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOper
   float wf[WS == WS_ROW && FINE ? Cfg::TN : 1][4];
   if constexpr (FINE && WS == WS_ROW) {
 #pragma unroll
-    for (int n = 0; n < Cfg::TN; ++n)
+    for (int n = 0; n < Cfg::TN; ++n) {
+      const float own = exp_byte((int)(sc.w[n] >> sc.shift) & 255);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) wf[n][v] = exp_byte(__shfl((int)(sc.w[n] >> sc.shift), 4 * (lane >> 4) + v) & 255);
+      for (int v = 0; v < 4; ++v) wf[n][v] = __shfl(own, 4 * (lane >> 4) + v);
+    }
   } else if constexpr (FINE) {
     wf[0][0] = WS == WS_F32 ? sc.f : exp_byte(sc.w_byte);
   }
@@ -564,7 +566,7 @@ hipError_t launch_mode(const ScaledArgs& a, int64_t rows, int64_t outs, hipStrea
     };
     const int64_t big = (tiles(256, 256) + 255) / 256 * 750, mid = tiles(128, 128) + 110;
     if constexpr (TALL) {
-      const bool brief = MODE == EXPERTS_GRAD && a.K <= (int64_t)1024 * a.E;
+      const bool brief = MODE == EXPERTS_GRAD && a.K <= (int64_t)1152 * a.E;      // 1024 rows and what fills their last block
       const int64_t tall = (tiles(128, 256) + 511) / 512 * (brief ? 700 : 825);
       if (tall < big && tall <= mid) return launch_cfg<Tall, MODE, WS, OUT_BF16>(a, s);
     }
