@@ -188,14 +188,15 @@ hipError_t launch_few_sized(const ScaledArgs& a, hipStream_t s) {
 // them once (16384 x 4096, M 32: 23 and 29).  Up to 16 rows read them once whatever
 // their width (28672 x 8192: 52 and 58 at M 1, 60 and 59 at M 16).
 //
-// Experts' workgroups are many, each of a stream as long as the contraction: with
-// 32 blocks or more this kernel wins up to 8 rows an expert (8 x 4096 x 4096, 4
-// each: 33 and 44; 64 x 1024 x 4096, 2 each: 55 and 57, 16 each: 86 and 67), with
-// fewer the tiles, if they fill the chip (64 x 4096 x 1024, 2 each: 73 and 58; 256
-// x 512 x 2048, 2 each: 69 and 51; but 32 x 512 x 2048, 4 each: 11.3 and 13.5).
+// Of experts at most M have rows.  With 32 blocks or more along the contraction
+// this kernel wins up to 8 rows an expert (8 x 4096 x 4096, 4 each: 33 and 44; 64 x
+// 1024 x 4096, 2 each: 55 and 57, 16 each: 86 and 67); with fewer, while its
+// workgroups, whose streams are short, are not many more than run at once (8 of 64 x
+// 4096 x 1024, one token: 12 and 18, 8 tokens: 50 and 47; 8 of 256 x 512 x 2048, one
+// token: 9 and 16, 8: 19 and 21, 2 rows each of all: 69 and 51).
 int scaled_few_tiles(int64_t M, int64_t N, int64_t blocks, int64_t E) {
   const int64_t across = (N + 31) / 32;
-  if (E) return M <= 8 * E && (blocks >= 32 || E * across <= 512) ? 1 : 0;
+  if (E) return M <= 8 * E && (blocks >= 32 || std::min(M, E) * across <= 2048) ? 1 : 0;
   const auto groups = [&](int tm) { return (M + 16 * tm - 1) / (16 * tm) * across; };
   if (M <= 16 || groups(1) <= 256) return 1;
   if (groups(2) <= (M <= 32 ? 512 : 256)) return 2;
