@@ -171,9 +171,11 @@ hipError_t launch_few(ScaledArgs a, hipStream_t s) {
 // (16 x 8 x 1024 x 8192: 15.5 against 16.6).
 template <int TM, int EXPERTS, int WS>
 hipError_t launch_few_sized(const ScaledArgs& a, hipStream_t s) {
-  const int64_t kbs = scale_blocks(a.K);
-  const bool eight = !EXPERTS && a.p * kbs >= 16 && (kbs <= 8 || a.N <= 2048);
-  return eight ? launch_few<TM, 2, 8, EXPERTS, WS>(a, s) : launch_few<TM, 2, 4, EXPERTS, WS>(a, s);
+  if constexpr (!EXPERTS) {
+    const int64_t kbs = scale_blocks(a.K);
+    if (a.p * kbs >= 16 && (kbs <= 8 || a.N <= 2048)) return launch_few<TM, 2, 8, EXPERTS, WS>(a, s);
+  }
+  return launch_few<TM, 2, 4, EXPERTS, WS>(a, s);
 }
 
 }  // namespace
