@@ -415,6 +415,7 @@ size_t tpf_qweight_matmul_ws(int p, int64_t M, int64_t K, int64_t N, int group);
  * A packed operand [M, K] is codes [M, K] and scales [M, S], S = ceil(K / 128)
  * rounded up to a multiple of 4: byte e of block b stands for 2^(e-127) (255: NaN),
  * so row m holds code[m][j] 2^(scales[m][j / 128] - 127).  K is a multiple of 16.
+ * The product of two blocks' scales has to lie within fp32's range.
  * ------------------------------------------------------------------------- */
 
 /* Scales of a weight's blocks of 128 x 128. */
