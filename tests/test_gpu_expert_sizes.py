@@ -116,6 +116,25 @@ def test_route_of_equal_logits(E, k, groups, tops, score, dtype):
         assert ((r.weights.cpu().double() - w).abs() <= w.abs() * (O.STEP + 2.0 ** -45)).all()
 
 
+@pytest.mark.parametrize("T,E,k", [(1, 5, 2), (200, 61, 8), (1100, 129, 8), (70, 250, 16), (40, 517, 9), (30, 1023, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_of_odd_numbers_of_experts(T, E, k, score, dtype, renorm):
+    """Rows of logits that start at any element; values past the last expert's belong to the next row."""
+    g = gen("odd", T, E)
+    x = (3 * torch.randn(T, E, generator=g)).to(dtype)
+    x[:, 0] += 4.0 * (torch.rand(T, generator=g) < 0.5).to(dtype)        # beside the end of the row before
+    for bias in (None, torch.randn(E, generator=g) * 0.2):
+        r = tp.expert_route(x.cuda(), k, score=score, renorm=renorm, bias=None if bias is None else bias.cuda())
+        ids = O.choose(x, k, score, bias, 1, 1, None)
+        assert torch.equal(r.ids.cpu(), ids)
+        for got, want in zip((r.offsets, r.src, r.pos), O.order(ids, E)):
+            assert torch.equal(got.cpu(), want)
+        w = O.route_weights(x, ids, score, renorm, 1.0)
+        assert ((r.weights.cpu().double() - w).abs() <= w.abs() * (O.STEP + 2.0 ** -45)).all()
+
+
 def test_two_graphs_share_a_workspace():
     T, E, k = 5000, 64, 4
     side = torch.cuda.Stream()
