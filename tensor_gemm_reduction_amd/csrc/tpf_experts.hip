@@ -342,7 +342,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
 // within the bound, a dozen values as a rule, goes into a list, and an entry's
 // place is the number of entries before it.  Where two entries lie closer than the
 // bound, places are taken from the list's values in 64 bits, and so are the groups
-// where the last taken and the first that is not lie so close; where more than 32
+// where one taken and one that is not lie so close; where more than 32
 // values reach the list or something is not finite, the token is routed again by
 // the whole wave in 64 bits: the choice is always the definition's.  Without bias
 // values are the logits themselves and nothing is uncertain.
@@ -376,11 +376,13 @@ union RouteLds {
   OrderLds order;
 };
 
-// Which groups are taken: lane g's `in` for group g, the least sum taken and the
-// largest that is not.  quads: LDS, the two largest of each four experts.
+// Which groups are taken: lane g's `in` for group g.  quads: LDS, the two largest of
+// each four experts.  Values v are off by up to slack / 2 (1 + |v|), and so are a
+// group's two largest, whose sum may be far smaller than they are; `sure`: the sums
+// taken lie above the others by more than that.
 template <int L, class T>
-__device__ __forceinline__ void choose_groups(const RouteArgs& a, const T (*quads)[2], int li, bool& in, T& worst,
-                                              T& next) {
+__device__ __forceinline__ void choose_groups(const RouteArgs& a, const T (*quads)[2], int li, T slack, bool& in,
+                                              bool& sure) {
   const T none = -(T)__builtin_huge_val();
   wave_lds();
   T t1 = none, t2 = none;
@@ -406,8 +408,11 @@ __device__ __forceinline__ void choose_groups(const RouteArgs& a, const T (*quad
   int place = 0;
   each_lane<16>(L == 16 ? mine : __shfl(mine, li & 15), [&](int g, T o) { place += o > mine || (o == mine && g < li); });
   in = li < a.groups && place < a.top_groups;
-  worst = min_over<L>(in ? mine : -none);
-  next = max_over<L>(in ? none : mine);
+  const T off = slack * (T(1) + fabs(t1) + fabs(t2));     // both values', the sum's rounding and that of what follows
+  T low = mine - off, high = mine + off;
+  if (!(low == low)) low = none;
+  if (!(high == high)) high = -none;
+  sure = min_over<L>(in ? low : -none) > max_over<L>(in || li >= a.groups ? none : high);
 }
 
 template <int L, int V, int F32>
@@ -430,7 +435,7 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
   // Twice the largest error of an fp32 value v is below bound (1 + |v|): sigmoid 4e-7 (exp2, reciprocal and sum
   // round by 1.2e-7 at most, the argument's rounding counts s (1 - s) |x| 2^-24), softmax 2.4e-6 (a sum of 1024).
   const float bound = !a.bias ? 0.0f : softmax ? 0x1p-17f : 0x1p-20f;
-  const float gbound = softmax ? 0x1p-16f : 0x1p-19f;
+  const float gslack = softmax ? 0x1p-17f : 0x1p-20f;
   const int t_end = min(a.T, (b + 1) * a.chunk);
   for (int t0 = b * a.chunk + wave * TOKENS; t0 < t_end; t0 += kRouteWaves * TOKENS) {
     // Hidden from the compiler, which would hold what follows from the lane's number in registers over the loop.
@@ -506,8 +511,7 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
             }
       }
       if (a.groups > 1) {
-        bool in;
-        float worst, next;
+        bool in, sure;
         float(*pairs)[2] = reinterpret_cast<float(*)[2]>(quads);
         wave_lds();
 #pragma unroll
@@ -517,10 +521,9 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
           pairs[four(q)][0] = max(a0, b0);
           pairs[four(q)][1] = max(min(a0, b0), max(a1, b1));
         }
-        choose_groups<L>(a, pairs, li, in, worst, next);
-        if (__ballot(a.top_groups < a.groups && !(worst - next > gbound * (1.0f + fabsf(worst))))) {
+        choose_groups<L>(a, pairs, li, gslack, in, sure);
+        if (__ballot(a.top_groups < a.groups && !sure)) {
           if (softmax && a.renorm) sum64 = softmax_sum<L, F32>(a, row, li, top64);
-          double worst64, next64;
           wave_lds();
 #pragma unroll 1
           for (int q = li; q < a.E / 4; q += L) {
@@ -535,7 +538,7 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
             quads[q][0] = t1;
             quads[q][1] = t2;
           }
-          choose_groups<L>(a, quads, li, in, worst64, next64);
+          choose_groups<L>(a, quads, li, 0.0, in, sure);
         }
         const uint32_t allowed = (uint32_t)(__ballot(in) >> lane0) & 0xffffu;
 #pragma unroll

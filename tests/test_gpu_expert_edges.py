@@ -1,0 +1,41 @@
+"""Routing, gradients and products at the edges of their ranges, on the GPU against float64."""
+import pytest
+import torch
+
+import scaled_oracle as O
+from tensor_gemm_reduction_amd import tpfuse as tp
+from test_gpu_experts import cuda, gen
+
+pytestmark = pytest.mark.gpu
+D = torch.float64
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("E,groups,tops,k", [(32, 8, 3, 4), (256, 8, 4, 8), (1024, 16, 5, 8)])
+@pytest.mark.parametrize("size", [32.0, 1000.0, 1e4])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_of_biases_that_cancel(E, groups, tops, k, size, score):
+    """A group's two largest near +B and -B, their sum near 1: the sum's error is that of its terms."""
+    T, n = 16384 if E < 1024 else 4096, E // groups
+    g = gen("cancel", E, size)
+    # from equal sums to sums that a step of fp32 near B tells apart
+    x = torch.randn(T, 1, generator=g) + torch.randn(T, E, generator=g) * torch.exp2(-24.0 * torch.rand(T, 1, generator=g))
+    bias = torch.full((E,), -4.0 * size)
+    bias[::n], bias[1::n] = size, -size
+    r = tp.expert_route(x.cuda(), k, score=score, bias=bias.cuda(), groups=groups, top_groups=tops)
+    biased = O.scores(x, score) + bias.to(D)
+    each = biased.view(T, groups, n)
+    total = each.topk(2, dim=2).values.sum(2)
+    ranked = torch.sort(total, dim=1, descending=True, stable=True)
+    best = ranked.indices[:, :tops]
+    allowed = torch.zeros(T, groups, dtype=torch.bool).scatter_(1, best, True)
+    value = torch.where(allowed[:, :, None], each, float("-inf")).view(T, E)
+    ids = torch.sort(value, dim=1, descending=True, stable=True).indices[:, :k]
+    # Scores whose last bits differ (exp, the softmax's sum) move s + B by a step of B, up to 2^-52 B, at most: a sum of
+    # two by two steps, two sums by four.  Sums that lie closer are decided by those last bits.
+    decided = ranked.values[:, tops - 1] - ranked.values[:, tops] > 4 * 2.0 ** -52 * size
+    assert decided.float().mean() > 0.5
+    assert torch.equal(r.ids.cpu()[decided], ids.to(torch.int32)[decided])
