@@ -509,6 +509,9 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
               for (int i = 0; i < 3; ++i)
                 if (four(q) * 4 + i < a.E) v[4 * q + i] += a.bias[four(q) * 4 + i];
             }
+        // a bias that is NaN: what follows counts on values that are ordered
+#pragma unroll
+        for (int i = 0; i < V; ++i) lost |= !(v[i] == v[i]);
       }
       if (a.groups > 1) {
         bool in, sure;

@@ -39,3 +39,21 @@ def test_groups_of_biases_that_cancel(E, groups, tops, k, size, score):
     decided = ranked.values[:, tops - 1] - ranked.values[:, tops] > 4 * 2.0 ** -52 * size
     assert decided.float().mean() > 0.5
     assert torch.equal(r.ids.cpu()[decided], ids.to(torch.int32)[decided])
+
+
+@pytest.mark.parametrize("E,k,groups,tops,at", [
+    (32, 4, 8, 2, range(1, 32, 4)), (256, 8, 8, 4, range(3, 256, 32)), (1024, 8, 16, 3, range(0, 1024, 64)),
+    (64, 16, 1, 1, range(8, 12)), (64, 16, 1, 1, range(0, 4)), (61, 16, 1, 1, range(56, 61)), (256, 16, 1, 1, range(16)),
+    (1024, 16, 1, 1, range(4, 1000)), (16, 12, 1, 1, range(5)), (64, 3, 1, 1, range(64)), (32, 6, 4, 2, range(8, 16))])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_with_biases_of_no_number(E, k, groups, tops, at, score):
+    """NaN counts as the least: in a group's sum, beside others, and where fewer than k others remain."""
+    g = gen("nan bias", E, k)
+    x = torch.randn(90, E, generator=g)
+    bias = torch.randn(E, generator=g) * 0.1
+    bias[list(at)] = float("nan")
+    r = tp.expert_route(x.cuda(), k, score=score, bias=bias.cuda(), groups=groups, top_groups=tops)
+    ids = O.choose(x, k, score, bias, groups, tops, None)
+    assert torch.equal(r.ids.cpu(), ids)
+    for got, want in zip((r.offsets, r.src, r.pos), O.order(ids, E)):
+        assert torch.equal(got.cpu(), want)
