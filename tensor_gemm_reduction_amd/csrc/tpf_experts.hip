@@ -343,9 +343,13 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
 // place is the number of entries before it.  Where two entries lie closer than the
 // bound, places are taken from the list's values in 64 bits, and so are the groups
 // where one taken and one that is not lie so close; where more than 32
-// values reach the list or something is not finite, the token is routed again by
-// the whole wave in 64 bits: the choice is always the definition's.  Without bias
-// values are the logits themselves and nothing is uncertain.
+// values reach the list, fewer than k do or something is not finite, the token is
+// routed again by the whole wave in 64 bits: the choice is always the definition's.
+// Without bias values are the logits themselves and nothing is uncertain.  Where fewer
+// than k lanes hold an expert that can be chosen (k above the fours of E or of the
+// groups taken), every finite value reaches the list: up to 32 of them that is the fast
+// way still (choice and order of 16384 tokens to 8 of 16: 14 us, in 64 bits 48), with
+// more experts (k from 14 on of 60: 55 to 78 us) it is not.
 // 16384 tokens, 256 experts in 8 groups with bias: 88 us with everything in 64 bits
 // and a round over all values for each choice, 20 this way (bound by the
 // instructions of about 2000 cycles a wave and by their first fetch).
@@ -428,8 +432,8 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
   __syncthreads();
   const bool softmax = a.score == SCORE_SOFTMAX, scores = a.bias || a.groups > 1;
   const int gs = a.E / a.groups, gs_inv = ((1 << 20) + gs - 1) / gs;
-  // Groups of whole fours take the fast way, and any number of experts without groups; other groups are routed in 64
-  // bits by the whole wave (16384 tokens: 6 of 128 17 us, of 129 by single loads 19, in 64 bits 47; 6 of 64 in 4
+  // Groups of whole fours take the fast way, and any number of experts without groups (but see k above); other groups
+  // are routed in 64 bits by the whole wave (16384 tokens: 6 of 128 17 us, of 129 by single loads 19, in 64 bits 47; 6 of 64 in 4
   // groups 17, of 60 49).
   const bool whole = a.E % 4 == 0, fours = a.groups == 1 || (whole && gs % 4 == 0);
   // Twice the largest error of an fp32 value v is below bound (1 + |v|): sigmoid 4e-7 (exp2, reciprocal and sum
@@ -570,14 +574,13 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
       each_lane<L>(m, [&](int j, float o) { place += o > m || (o == m && j < li); });
       const uint64_t kth = __ballot(place == a.k - 1) >> lane0 & (L == 64 ? ~0ull : (1ull << L) - 1);
       float least = __shfl(m, lane0 + (kth ? __builtin_ctzll(kth) : 0));
-      least -= 2.0f * bound * (1.0f + fabsf(least));
-      lost |= !(least > -__builtin_huge_valf());
+      least = max(least - 2.0f * bound * (1.0f + fabsf(least)), -0x1.fffffep127f);     // fewer lanes: all that is finite
       int n = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) n += v[i] >= least;
       const int upto = sum_upto<L>(n, li);
       const int total = max_over<L>(upto);
-      lost |= total > LIST;
+      lost |= total > LIST || total < a.k;
       int at = upto - n;
       wave_lds();
 #pragma unroll

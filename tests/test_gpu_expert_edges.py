@@ -4,7 +4,7 @@ import torch
 
 import scaled_oracle as O
 from tensor_gemm_reduction_amd import tpfuse as tp
-from test_gpu_experts import cuda, gen
+from test_gpu_experts import F32, cuda, gen, weights
 
 pytestmark = pytest.mark.gpu
 D = torch.float64
@@ -57,3 +57,27 @@ def test_route_with_biases_of_no_number(E, k, groups, tops, at, score):
     assert torch.equal(r.ids.cpu(), ids)
     for got, want in zip((r.offsets, r.src, r.pos), O.order(ids, E)):
         assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("E,k,groups,tops", [(8, 3, 1, 1), (8, 8, 1, 1), (16, 8, 1, 1), (31, 16, 1, 1), (32, 16, 1, 1),
+                                             (60, 16, 1, 1), (16, 5, 4, 2), (256, 16, 8, 1), (64, 10, 4, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_to_more_experts_than_lanes_hold(E, k, groups, tops, score, biased):
+    """More experts a token than there are fours of them to choose from."""
+    g = gen("few fours", E, k)
+    x = torch.randn(70, E, generator=g)
+    x[1] = 0.0
+    x[2, k - 1:] = float("-inf")              # fewer than k that are not masked
+    x[3, k:] = float("-inf")
+    x[4, k - 1:] = torch.finfo(F32).min
+    x[5] = torch.finfo(F32).min
+    x[6] = torch.arange(E) // 2 % 5
+    x[7, 0] = torch.finfo(F32).max
+    bias = torch.randn(E, generator=g) * 0.1 if biased else None
+    r = tp.expert_route(x.cuda(), k, score=score, bias=None if bias is None else bias.cuda(), groups=groups,
+                        top_groups=tops)
+    ids = O.choose(x, k, score, bias, groups, tops, None)
+    assert torch.equal(r.ids.cpu(), ids)
+    w = O.route_weights(x, ids, score, True, 1.0)
+    assert ((r.weights.cpu().to(D) - w).abs() <= w.abs() * (O.STEP + 2.0 ** -40) + 2.0 ** -149).all()
