@@ -480,7 +480,8 @@ int tpf_scaled_weight_grad(tpf_handle h, int p, int64_t Mt, int64_t R, int64_t C
  * largest sums of their two largest s + bias can be chosen.
  *   ids: [T, k], -1 for tokens that are not routed.
  *   weights: [T, k] fp32: scale * s of the chosen, with renorm != 0 divided by
- *   their sum (0 where that is 0); 0 for tokens that are not routed.
+ *   their sum (0 where that is 0); 0 for tokens that are not routed.  A NaN or
+ *   +inf among a token's logits makes its softmax and so its weights NaN.
  *   offsets: [E + 1], expert e's rows are offsets[e] .. offsets[e+1] - 1.
  *   src: [T k], the slot of each row, -1 behind the last row.
  *   pos: [T, k], the row of each slot, -1 for tokens that are not routed.

@@ -230,7 +230,8 @@ __global__ __launch_bounds__(kRouteThreads) void expert_order_kernel(RouteArgs a
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 // A token's experts and weights once the choice is made: lane j < k of the L that
-// share the token holds the j-th expert.  top and sum: the softmax's (64 bits).
+// share the token holds the j-th expert.  top and sum: the softmax's (64 bits); a sum
+// of NaN makes the weights NaN.
 template <int L, int F32>
 __device__ __forceinline__ void put_choice(const RouteArgs& a, int t, int li, int id, bool routed, double top, double sum,
                                            int* hist) {
@@ -239,6 +240,7 @@ __device__ __forceinline__ void put_choice(const RouteArgs& a, int t, int li, in
   if (mine) {
     const double l = value_at<F32>(a.logits, (int64_t)t * a.E + id);
     s = a.score == SCORE_SIGMOID ? sigmoid64(l) : (top == kNone ? 0.0 : exp(l - top));
+    if (!(sum == sum)) s = sum;
   }
   if (a.renorm) sum = sum_over<L>(s);
   if (li < a.k) {
@@ -267,15 +269,24 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
   const bool softmax = a.score == SCORE_SOFTMAX, scores = a.bias || a.groups > 1;
   double top = kNone, sum = 1.0;
 #pragma unroll 1
-  for (int e = lane; e < a.E; e += 64) top = max(top, (double)value_at<F32>(a.logits, row + e));
+  for (int e = lane; e < a.E; e += 64) {
+    const double l = value_at<F32>(a.logits, row + e);
+    if (!(l == l)) sum = l;
+    top = max(top, l);
+  }
   top = max_over<64>(top);
-  if (softmax && (scores || !a.renorm)) sum = top == kNone ? 0.0 : softmax_sum<64, F32>(a, row, lane, top);
+  if (softmax) {                    // over a NaN or +inf it is NaN throughout, renormalised or not
+    if (__ballot(!(sum == sum)) || top == -kNone) sum = __builtin_nan("");
+    else if (scores || !a.renorm) sum = top == kNone ? 0.0 : softmax_sum<64, F32>(a, row, lane, top);
+  } else {
+    sum = 1.0;
+  }
   wave_lds();
 #pragma unroll 1
   for (int e = lane; e < a.E; e += 64) {
     const double l = value_at<F32>(a.logits, row + e);
     double v = l;
-    if (scores) v = softmax ? (top == kNone ? 0.0 : exp(l - top) / sum) : sigmoid64(l);
+    if (scores) v = softmax ? (sum == 0.0 ? 0.0 : exp(l - top) / sum) : sigmoid64(l);
     if (a.bias) v += (double)a.bias[e];
     values[e] = v == v ? v : kNone;
   }

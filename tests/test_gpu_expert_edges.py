@@ -81,3 +81,18 @@ def test_route_to_more_experts_than_lanes_hold(E, k, groups, tops, score, biased
     assert torch.equal(r.ids.cpu(), ids)
     w = O.route_weights(x, ids, score, True, 1.0)
     assert ((r.weights.cpu().to(D) - w).abs() <= w.abs() * (O.STEP + 2.0 ** -40) + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("E", [8, 64, 130, 1024])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_softmax_of_no_number(E, biased, renorm):
+    """A softmax over NaN or +inf is NaN throughout: so are the weights, of those tokens alone."""
+    x = torch.randn(20, E, generator=gen("nan logit", E))
+    x[3, 5] = float("nan")
+    x[7, 2] = float("inf")
+    bias = torch.linspace(-0.1, 0.1, E) if biased else None
+    r = tp.expert_route(x.cuda(), 2, renorm=renorm, bias=None if bias is None else bias.cuda())
+    bad = torch.zeros(20, 2, dtype=torch.bool)
+    bad[[3, 7]] = True
+    assert torch.equal(r.weights.cpu().isnan(), bad)
