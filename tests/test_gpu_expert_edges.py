@@ -4,7 +4,7 @@ import torch
 
 import scaled_oracle as O
 from tensor_gemm_reduction_amd import tpfuse as tp
-from test_gpu_experts import F32, cuda, gen, weights
+from test_gpu_experts import BF, F32, cuda, gen, weights
 
 pytestmark = pytest.mark.gpu
 D = torch.float64
@@ -96,3 +96,48 @@ def test_softmax_of_no_number(E, biased, renorm):
     bad = torch.zeros(20, 2, dtype=torch.bool)
     bad[[3, 7]] = True
     assert torch.equal(r.weights.cpu().isnan(), bad)
+
+
+# ---------------------------------------------------------------------------
+# the router's gradient
+# ---------------------------------------------------------------------------
+
+def confident(T, E, k, dtype):
+    """Logits with one expert 8 to 14 above the others."""
+    g = gen("confident", T, E, k)
+    x = 0.5 * torch.randn(T, E, generator=g)
+    x[torch.arange(T), torch.randint(E, (T,), generator=g)] = torch.linspace(8.0, 14.0, T) + 1.0
+    return x.to(dtype), torch.randn(T, k, generator=g)
+
+
+@pytest.mark.parametrize("T,E,k", [(60, 2, 1), (60, 2, 2), (70, 8, 1), (70, 64, 2), (65, 100, 3), (40, 1024, 1), (40, 1024, 16)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradient_of_a_confident_softmax(T, E, k, dtype):
+    """Without renormalisation: s (1 - s) keeps its bits where s is close to 1."""
+    x, dw = confident(T, E, k, dtype)
+    mask = torch.arange(T) % 7 != 3
+    r = tp.expert_route(x.cuda(), k, renorm=False, scale=1.7, mask=mask.cuda())
+    d = tp.expert_route_backward(dw.cuda(), x.cuda(), r, renorm=False, scale=1.7).cpu().to(D)
+    leaf = x.to(D).requires_grad_()
+    at = r.ids.cpu().clamp(min=0).long()
+    (torch.gather(torch.softmax(leaf, 1), 1, at) * 1.7 * dw.to(D) * mask[:, None]).sum().backward()
+    # The terms' size without what cancels: at a chosen one 1 - s of its own and the others' s.
+    s = torch.softmax(x.to(D), 1)
+    one = torch.zeros(T, E, dtype=D).scatter_(1, at, 1.7 * dw.abs().to(D))
+    total = (s * one).sum(1, keepdim=True)
+    size = s * (one * (1.0 - s) + (total - s * one)) + s * total * (one == 0)
+    # everything in 64 bits (the reference's 1 - s loses 2^-52 of 1), one rounding to fp32 and one to the result's type
+    tol = leaf.grad.abs() * (O.half_step(dtype) + O.STEP) + size * 2.0 ** -40 + s * one * 2.0 ** -50
+    assert ((d - leaf.grad).abs() <= tol + 2.0 ** -149).all()
+    assert (d[~mask] == 0).all()
+
+
+def test_gradient_of_a_softmax_of_no_number():
+    x = torch.randn(8, 64, generator=gen("no number")).cuda()
+    x[1, 7] = x[2] = float("nan")
+    x[3, 9] = float("inf")
+    x[4] = x[5, 1:] = float("-inf")
+    r = tp.expert_route(x, 2, renorm=False)
+    d = tp.expert_route_backward(torch.ones(8, 2).cuda(), x, r, renorm=False).cpu()
+    assert torch.equal(d.isnan().all(1), torch.tensor([0, 1, 1, 1, 0, 0, 0, 0], dtype=torch.bool))
+    assert (d[4:6] == 0).all() and d[[0, 6, 7]].isfinite().all()
