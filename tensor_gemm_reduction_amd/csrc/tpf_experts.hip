@@ -673,7 +673,9 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
 }
 
 // The router's gradient.  Through renormalised weights w = c s / sum s it is
-// dl = w (dw - sum_i w_i dw_i / c), times 1 - s for sigmoid scores; otherwise
+// dl = w (dw - sum_i w_i dw_i / c), times 1 - s for sigmoid scores.  The weights sum to
+// c, so that is w sum_i w_i (dw - dw_i) / c, which does not cancel where one weight is
+// close to c and its difference to c lost in its rounding to fp32.  Otherwise
 // dl = w dw (1 - s) through w = c s of a sigmoid: nothing but the chosen experts'
 // logits matter.  16 lanes take a token's choices and lay its row out in LDS, so that
 // the gradient is written once, whole (16384 tokens, 256 experts: 7 us; with a wave a
@@ -690,7 +692,7 @@ __global__ __launch_bounds__(256) void expert_route_backward_kernel(RouteGradArg
     const int64_t t = t0 + tok;
     for (int e = li * 4; e < width; e += 64) *reinterpret_cast<f32x4_t*>(mine + e) = f32x4_t{0, 0, 0, 0};
     int id = -1;
-    double w = 0.0, g = 0.0;
+    float w = 0.0f, g = 0.0f;
     if (t < a.T && li < a.k) {
       id = a.ids[t * a.k + li];
       if ((uint32_t)id >= (uint32_t)a.E) id = -1;
@@ -699,8 +701,15 @@ __global__ __launch_bounds__(256) void expert_route_backward_kernel(RouteGradArg
         g = a.dweights[t * a.k + li];
       }
     }
-    const double total = sum_over<16>(w * g);
-    double d = a.renorm ? w * (g - total / a.scale) : w * g;
+    double d = g;
+    if (a.renorm) {
+      double sum = 0.0;
+      each_lane<16>((uint64_t)__float_as_uint(g) << 32 | __float_as_uint(w), [&](int, uint64_t o) {
+        sum += (double)__uint_as_float((uint32_t)o) * ((double)g - (double)__uint_as_float((uint32_t)(o >> 32)));
+      });
+      d = sum / a.scale;
+    }
+    d *= w;
     if (a.score == SCORE_SIGMOID && id >= 0) d = d / (1.0 + exp((double)value_at<F32>(a.logits, t * a.E + id)));
     wave_lds();
     if (id >= 0) mine[id] = (float)d;

@@ -141,3 +141,27 @@ def test_gradient_of_a_softmax_of_no_number():
     d = tp.expert_route_backward(torch.ones(8, 2).cuda(), x, r, renorm=False).cpu()
     assert torch.equal(d.isnan().all(1), torch.tensor([0, 1, 1, 1, 0, 0, 0, 0], dtype=torch.bool))
     assert (d[4:6] == 0).all() and d[[0, 6, 7]].isfinite().all()
+
+
+@pytest.mark.parametrize("T,E,k", [(60, 2, 2), (70, 64, 2), (65, 100, 3), (40, 1024, 16)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_gradient_of_confident_weights(T, E, k, score, dtype):
+    """Renormalised weights, one close to 1: w_j (1 - w_j) keeps its bits."""
+    x, dw = confident(T, E, k, dtype)
+    if score == "sigmoid":
+        x = (x.float() - 13.0).to(dtype)
+    r = tp.expert_route(x.cuda(), k, score=score, scale=1.7)
+    d = tp.expert_route_backward(dw.cuda(), x.cuda(), r, score=score, scale=1.7).cpu().to(D)
+    leaf = x.to(D).requires_grad_()
+    at = r.ids.cpu().long()
+    w = torch.gather(O.scores(leaf, score), 1, at)
+    w = 1.7 * w / w.sum(1, keepdim=True)
+    (w * dw.to(D)).sum().backward()
+    # w_j sum_i w_i (g_j - g_i) / scale: each weight was rounded to fp32; sums in 64 bits; a rounding to fp32 and one
+    # to the result's type
+    v = w.detach()
+    apart = (dw.to(D)[:, :, None] - dw.to(D)[:, None, :]).abs()
+    size = torch.zeros(T, E, dtype=D).scatter_(1, at, v * (v[:, None, :] * apart).sum(2) / 1.7)
+    tol = leaf.grad.abs() * (O.half_step(dtype) + O.STEP) + size * 2.01 * O.STEP + 2.0 ** -50
+    assert ((d - leaf.grad).abs() <= tol).all()
