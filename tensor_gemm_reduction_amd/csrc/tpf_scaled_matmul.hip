@@ -4,8 +4,10 @@
 // v_mfma_scale_f32_16x16x128 multiplies 16 x 128 codes by 128 x 16 and applies
 // a power of two to each operand's block: exactly one block of 128, so packed
 // rows' exponent bytes go into the instruction and a product of two of them
-// costs nothing beside it.  Weights with fp32 scales take the block's partial
-// sum from the instruction and one fused multiply-add an element more.
+// costs nothing beside it.  Of a weight's fp32 scale the power of two goes into the
+// instruction as well, so that no partial sum leaves fp32's range where the scales'
+// product lies within it (4096^3: 97 us as with the whole scale afterwards); its other
+// part, 1 to 2, takes one fused multiply-add an element more.
 //
 // Lane l of the instruction holds 32 codes of row (or column) l % 16.  Which 32
 // of the block's 128 each group of 16 lanes holds is free, as long as both
@@ -155,6 +157,17 @@ struct ScLoader {
                                              (int)within(w_off[i], Cfg::W_LOADS % 2 ? q : i, K), k0, 0, 0);
   }
 };
+
+// An fp32 factor as the byte of its power of two and what is left: +-[1, 2), [0, 2)
+// below the least normal number, infinities and NaN as they are.
+struct ScFactor {
+  int byte;
+  float part;
+};
+__device__ __forceinline__ ScFactor sc_factor(float f) {
+  const int byte = min((int)(__float_as_uint(f) >> 23 & 255), 254);
+  return ScFactor{byte, __builtin_amdgcn_ldexpf(f, 127 - byte)};
+}
 
 // A wave's scales.  Lane l loads the word of row l (and l + 64), four blocks'
 // exponent bytes; rows of 16 lanes then spread over the wave, so that lane l
@@ -323,6 +336,8 @@ __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOper
   } else if constexpr (FINE) {
     wf[0][0] = WS == WS_F32 ? sc.f : exp_byte(sc.w_byte);
   }
+  ScFactor factor{};
+  if constexpr (!FINE && WS == WS_F32) factor = sc_factor(sc.f);
   if constexpr (!ONE) ld.next(a, kbs);
 #pragma unroll
   for (int s = 0; s < S; ++s) {
@@ -354,9 +369,9 @@ __device__ __forceinline__ void sc_step(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOper
           for (int v = 0; v < 4; ++v)
             acc[m][n][v] = __builtin_fmaf(part[v], xs * (WS == WS_ROW ? wf[n][v] : wf[0][0]), acc[m][n][v]);
         } else if constexpr (WS == WS_F32) {
-          const f32x4_t part = sc_mfma(o.w[n], o.x[s & 1][i], f32x4_t{0, 0, 0, 0}, 127, (int)xb);
+          const f32x4_t part = sc_mfma(o.w[n], o.x[s & 1][i], f32x4_t{0, 0, 0, 0}, factor.byte, (int)xb);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[m][n][v] = __builtin_fmaf(part[v], sc.f, acc[m][n][v]);
+          for (int v = 0; v < 4; ++v) acc[m][n][v] = __builtin_fmaf(part[v], factor.part, acc[m][n][v]);
         } else {
           acc[m][n] = sc_mfma(o.w[n], o.x[s & 1][i], acc[m][n],
                               (int)(WS == WS_ROW ? sc.w[n] >> sc.shift : sc.w_byte), (int)xb);

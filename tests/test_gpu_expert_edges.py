@@ -4,7 +4,7 @@ import torch
 
 import scaled_oracle as O
 from tensor_gemm_reduction_amd import tpfuse as tp
-from test_gpu_experts import BF, F32, cuda, gen, weights
+from test_gpu_experts import BF, F8, F32, U8, cuda, gen, integer_packed, route_of, weights
 
 pytestmark = pytest.mark.gpu
 D = torch.float64
@@ -165,3 +165,86 @@ def test_gradient_of_confident_weights(T, E, k, score, dtype):
     size = torch.zeros(T, E, dtype=D).scatter_(1, at, v * (v[:, None, :] * apart).sum(2) / 1.7)
     tol = leaf.grad.abs() * (O.half_step(dtype) + O.STEP) + size * 2.01 * O.STEP + 2.0 ** -50
     assert ((d - leaf.grad).abs() <= tol).all()
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+
+def extreme(g, M, K, N, kind, E=0):
+    """Integer operands, scales at both ends that multiply out: (x, xs, w, ws, which results are in range)."""
+    (x,), (xs,) = integer_packed(g, M, K, 1)
+    (w,), (ws,) = weights(g, 1, ((E,) if E else ()) + (N, K), "f32" if kind == "f32" else "u8", integer=True)
+    row = torch.tensor([252, 2, 127, 100])[torch.arange(M) % 4]
+    xs[:] = row[:, None].to(U8)
+    block = torch.tensor([2, 252, 127, 154])[torch.arange(O.blocks(N)) % 4]
+    if kind == "u8":
+        ws[:] = block[:, None].to(U8)
+    else:           # 1 to 3 times the power of two, one in five of them negative
+        sign = torch.where(torch.rand(ws.shape, generator=g) < 0.2, -1.0, 1.0)
+        ws.copy_(ws * sign * torch.exp2(block.float() - 127.0)[:, None])
+    column = torch.repeat_interleave(block, 128)[:N]
+    return x, xs, w, ws, (row[:, None] + column[None, :] - 254).abs() <= 14
+
+
+# few rows; tiles of 128 x 128; of 256 x 256 (powers of two, bf16)
+@pytest.mark.parametrize("M,K,N", [(9, 272, 520), (40, 144, 520), (700, 272, 1032), (3600, 144, 3592)])
+@pytest.mark.parametrize("kind", ["u8", "f32"])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_extreme_scales_of_products(M, K, N, kind, out):
+    x, xs, w, ws, ok = extreme(gen("ends", M), M, K, N, kind)
+    y = tp.fp8_matmul([x.cuda()], [xs.cuda()], [w.cuda()], [ws.cuda()], out_dtype=out).cpu()
+    want = (O.values(x, xs) @ O.weight(w, ws).t()).to(out)
+    assert torch.equal(y[ok], want[ok])
+
+
+@pytest.mark.parametrize("T,E,k,K,N", [(40, 5, 2, 144, 520), (4000, 3, 2, 144, 1032), (3000, 60, 4, 144, 1032)])
+@pytest.mark.parametrize("kind", ["u8", "f32"])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_extreme_scales_of_experts(T, E, k, K, N, kind, out):
+    g = gen("ends", T, E)
+    r = route_of(g, T, E, k)
+    x, xs, w, ws, ok = extreme(g, T * k, K, N, kind, E)
+    y = tp.expert_matmul([x.cuda()], [xs.cuda()], [w.cuda()], [ws.cuda()], tp.ExpertRoute(*(t.cuda() for t in r)),
+                         out_dtype=out).cpu()
+    xv = O.values(x, xs)
+    for e in range(E):
+        at = slice(int(r.offsets[e]), int(r.offsets[e + 1]))
+        want = (xv[at] @ O.weight(w[e], ws[e]).t()).to(out)
+        assert torch.equal(y[at][ok[at]], want[ok[at]])
+
+
+@pytest.mark.parametrize("R,C", [(264, 392), (3600, 3592)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_extreme_scales_of_weight_gradients(R, C, out):
+    g = gen("ends", R)
+    (a,), (as_,) = integer_packed(g, R, 256, 1)
+    (b,), (bs,) = integer_packed(g, C, 256, 1)
+    row, col = torch.tensor([252, 2, 127, 100])[torch.arange(R) % 4], torch.tensor([2, 252, 127])[torch.arange(C) % 3]
+    as_[:], bs[:] = row[:, None].to(U8), col[:, None].to(U8)
+    ok = (row[:, None] + col[None, :] - 254).abs() <= 14
+    dw = tp.fp8_weight_grad([a.cuda()], [as_.cuda()], [b.cuda()], [bs.cuda()], out_dtype=out)[0].cpu()
+    want = (O.values(a, as_) @ O.values(b, bs).t()).to(out)
+    assert torch.equal(dw[ok], want[ok])
+
+
+@pytest.mark.parametrize("M,K,N", [(9, 128, 520), (700, 128, 1032)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_factors_that_are_special(M, K, N, out):
+    """fp32 scales of zero, below the least normal number, infinite and NaN, each in its own columns."""
+    g = gen("special", M)
+    (x,), (xs,), (w,), (ws,) = *integer_packed(g, M, K, 1), *weights(g, 1, (N, K), "f32", integer=True)
+    sign = torch.where(torch.arange(M)[:, None] % 2 == 0, 1.0, -1.0)
+    x, w = (sign * x.float().abs().clamp(min=1.0)).to(F8), w.float().abs().clamp(min=1.0).to(F8)    # no sum is 0
+    xs[:] = 127
+    xs[1] = 250
+    factors = (1.0, 0.0, 3 * 2.0 ** -140, float("inf"), float("nan"))
+    ws[:5, 0] = torch.tensor(factors)
+    y = tp.fp8_matmul([x.cuda()], [xs.cuda()], [w.cuda()], [ws.cuda()], out_dtype=out).cpu()
+    part = O.values(x, xs) @ w.to(D).t()
+    for i, f in enumerate(factors):
+        at = slice(128 * i, min(128 * (i + 1), N))
+        want = (part[:, at] * f).to(out)
+        rows = [1] if f == 3 * 2.0 ** -140 else [m for m in range(M) if m != 1 or i == 1]   # results below fp32's range
+        assert torch.equal(y[rows][:, at].nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30),
+                           want[rows].nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30))
