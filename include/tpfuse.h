@@ -410,13 +410,24 @@ size_t tpf_qweight_matmul_ws(int p, int64_t M, int64_t K, int64_t N, int group);
 
 /* ---------------------------------------------------------------------------
  * Linears in 8 bits.  Operands are OCP e4m3 codes with a scale for each block of
- * 128 along the contraction; sums are fp32.  Conventions as above.
+ * 128 along the contraction.  Conventions as above.
+ *
+ * Sums.  fp32 results are sums in fp32.  bf16 results of more than a few rows, and
+ * weight gradients in bf16, are summed by the 8-bit matrix instructions, which add
+ * eight products at a time with 13 binary places below the largest of the eight:
+ * before the rounding to bf16 they may be off by 2^-10 of the sum of the products'
+ * magnitudes (about 2^-16 as a rule), and where products cancel by all of the
+ * result.  With y_dtype or dw_dtype TPF_BF16 | TPF_SUMS_F32 they are sums in fp32
+ * as well, in about twice the time, whatever the number of rows.
  *
  * A packed operand [M, K] is codes [M, K] and scales [M, S], S = ceil(K / 128)
  * rounded up to a multiple of 4: byte e of block b stands for 2^(e-127) (255: NaN),
  * so row m holds code[m][j] 2^(scales[m][j / 128] - 127).  K is a multiple of 16.
  * The product of two blocks' scales has to lie within fp32's range.
  * ------------------------------------------------------------------------- */
+
+/* Added to a call's y_dtype or dw_dtype: sums in fp32 whatever the result's type. */
+#define TPF_SUMS_F32 0x100
 
 /* Scales of a weight's blocks of 128 x 128. */
 #define TPF_SCALE_BYTE 0         /* bytes, 2^(e-127), 255: NaN */

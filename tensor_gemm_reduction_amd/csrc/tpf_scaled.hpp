@@ -73,6 +73,7 @@ struct ScaledArgs {
   int xsw, wsw;
   int E, top;                        // top: slots a token where x's rows are tokens (0: x's rows are the result's)
   int gelu, out;
+  int fine;                          // sums in fp32 whatever the result's type
   int tiles_m, tiles_n, tasks;
 };
 // Tiles of 16 rows that the kernel for few rows takes for M rows (of E experts),

@@ -135,6 +135,8 @@ int scaled_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, int64_t 
     if ((st = check_ints(offsets, "offsets"))) return st;
   }
   if ((st = check_scale_type(w_scale_type))) return st;
+  const int fine = y_dtype & TPF_SUMS_F32;
+  y_dtype -= fine;
   if (!valid_dtype(y_dtype)) return fail(TPF_ERR_INVALID_ARG, "unknown output dtype");
   if ((st = check_ptrs(X, p, "X"))) return st;
   if ((st = check_ptrs_at(x_scales, p, "x_scales", 4))) return st;
@@ -157,6 +159,7 @@ int scaled_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, int64_t 
   a.src = src;
   a.gelu = gelu;
   a.out = out_kind(y_dtype);
+  a.fine = fine;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   TPF_TIMED(h, s, launch_scaled_matmul(a, w_scale_type, s));
   return TPF_OK;
@@ -172,6 +175,8 @@ int scaled_weight_grad(tpf_handle h, int p, int64_t Mt, int64_t R, int64_t C, in
   if ((st = check_packed(C, Mt, "C and Mt"))) return st;
   if ((st = check_product(R, C, (int64_t)p * (E ? E : 1)))) return st;
   if (E && (st = check_ints(offsets, "offsets"))) return st;
+  const int fine = dw_dtype & TPF_SUMS_F32;
+  dw_dtype -= fine;
   if (!valid_dtype(dw_dtype)) return fail(TPF_ERR_INVALID_ARG, "unknown output dtype");
   if ((st = check_ptrs(A, p, "A"))) return st;
   if ((st = check_ptrs_at(a_scales, p, "a_scales", 4))) return st;
@@ -190,6 +195,7 @@ int scaled_weight_grad(tpf_handle h, int p, int64_t Mt, int64_t R, int64_t C, in
   a.E = (int)E;
   a.offsets = offsets;
   a.out = out_kind(dw_dtype);
+  a.fine = fine;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   TPF_TIMED(h, s, launch_scaled_weight_grad(a, s));
   return TPF_OK;

@@ -16,9 +16,11 @@
 //
 // The 8-bit instructions add eight products at a time with 13 binary places
 // below the largest of the eight and drop the rest (measured; all forms of them
-// do): about 2^-16 of a sum's size, far below half a step of bf16 (2^-9), so
-// results in bf16 take them.  Results in fp32 take the bf16 instructions, at
-// half the rate: codes are exact in bf16 and those sums keep fp32's bits.
+// do): less than 2^-10 of the products' magnitudes, about 2^-16 of them as a rule,
+// far below half a step of bf16 (2^-9) unless products cancel, so results in bf16
+// take them.  Results in fp32, and those in bf16 that are asked for with sums in
+// fp32 (FINE), take the bf16 instructions, at half the rate: codes are exact in
+// bf16 and those sums keep fp32's bits.
 //
 // What bounds them: 4 x 4096 x 4096 x 4096 take 201 us, 2730 TFLOP/s; the matrix
 // cores are busy 64 % of the time at the 1.9 GHz that the board holds them to (a
@@ -418,11 +420,10 @@ __device__ __forceinline__ void sc_steps(f32x4_t (&acc)[Cfg::TM][Cfg::TN], ScOpe
   }
 }
 
-template <class Cfg, int MODE, int WS, int OUT>
+template <class Cfg, int MODE, int WS, int OUT, int FINE>
 __global__ __launch_bounds__(Cfg::THREADS, 2) void scaled_tile_kernel(ScaledArgs args) {
   (void)args;
   const ScaledArgs& a = *(const ScaledArgs*)__builtin_amdgcn_kernarg_segment_ptr();
-  constexpr int FINE = OUT == OUT_F32;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane & 15;
   const int wm = wave / Cfg::WAVES_N, wn = wave % Cfg::WAVES_N;
   ScJob j{};
@@ -547,7 +548,7 @@ using Big = ScCfg<256, 256, 2, 4, 2>;
 using Tall = ScCfg<128, 256, 1, 4, 1>;
 using Mid = ScCfg<128, 128, 2, 2, 2>;
 
-template <class Cfg, int MODE, int WS, int OUT>
+template <class Cfg, int MODE, int WS, int OUT, int FINE = OUT == OUT_F32>
 hipError_t launch_cfg(ScaledArgs a, hipStream_t s) {
   a.tiles_n = (a.N + Cfg::BN - 1) / Cfg::BN;
   a.tiles_m = (a.M + Cfg::BM - 1) / Cfg::BM;
@@ -556,7 +557,7 @@ hipError_t launch_cfg(ScaledArgs a, hipStream_t s) {
   if (MODE == GRAD || MODE == EXPERTS_GRAD) tasks *= a.p * (MODE == EXPERTS_GRAD ? a.E : 1);
   if (tasks * Cfg::THREADS >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   a.tasks = (int)tasks;
-  hipLaunchKernelGGL((scaled_tile_kernel<Cfg, MODE, WS, OUT>), dim3(a.tasks), dim3(Cfg::THREADS), 0, s, a);
+  hipLaunchKernelGGL((scaled_tile_kernel<Cfg, MODE, WS, OUT, FINE>), dim3(a.tasks), dim3(Cfg::THREADS), 0, s, a);
   return hipGetLastError();
 }
 
@@ -580,6 +581,7 @@ hipError_t launch_cfg(ScaledArgs a, hipStream_t s) {
 template <int MODE, int WS>
 hipError_t launch_mode(const ScaledArgs& a, int64_t rows, int64_t outs, hipStream_t s) {
   if (a.out == OUT_F32) return launch_cfg<Mid, MODE, WS, OUT_F32>(a, s);
+  if (a.fine) return launch_cfg<Mid, MODE, WS, OUT_BF16, 1>(a, s);
   if constexpr (WS != WS_F32) {
     constexpr bool TALL = MODE == EXPERTS || MODE == EXPERTS_GRAD;
     const auto tiles = [&](int64_t bm, int64_t bn) {

@@ -31,6 +31,7 @@ OP_MATMUL_ALLREDUCE, OP_MATMUL_REDUCESCATTER, OP_ALLGATHER_MATMUL, OP_MATMUL_DX,
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 NORM_MAX_H = 32768
 SCALE_BYTE, SCALE_F32 = 0, 1
+SUMS_F32 = 0x100
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 EXPERT_MAX_E, EXPERT_MAX_K, EXPERT_MAX_GROUPS = 1024, 16, 16
 MAX_SHARDS = 16
@@ -980,6 +981,10 @@ def _scaled_weights(codes, scales, shape, dev):
     return at, SCALE_F32 if dtype == torch.float32 else SCALE_BYTE
 
 
+def _sum_code(dtype: torch.dtype, fp32_sums: bool) -> int:
+    return _dtype_code(dtype) | (SUMS_F32 if fp32_sums else 0)
+
+
 def _result(name: str, Y, dtype, shape, dev, stream):
     """The caller's output, or a new one."""
     if Y is None:
@@ -993,14 +998,21 @@ def _result(name: str, Y, dtype, shape, dev, stream):
 
 def fp8_matmul(X: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor], W: Sequence[torch.Tensor],
                w_scales: Sequence[torch.Tensor], gelu: bool = False, out_dtype=torch.bfloat16,
-               Y: Optional[torch.Tensor] = None, handle: Optional[Handle] = None, stream=None) -> torch.Tensor:
+               Y: Optional[torch.Tensor] = None, handle: Optional[Handle] = None, stream=None,
+               fp32_sums: bool = False) -> torch.Tensor:
     """Y = sum_k X[k] W_k^T in 8 bits (row-parallel over the shards; p = 1: any
     Linear), GeLU of it with `gelu`.
 
     X[k], x_scales[k]: [M, K] as `fp8_pack` leaves it; W[k] [N, K] e4m3 with a scale
     for each 128 x 128 block, w_scales[k] [ceil(N/128), ceil(K/128)]: fp32 factors,
     or uint8 powers of two 2^(w_scales - 127).  An input gradient is the same
-    product with the transposed weight."""
+    product with the transposed weight.
+
+    fp32 results are sums in fp32.  bf16 results of more than a few rows take the
+    8-bit matrix instructions' sums, which keep 13 binary places below the largest of
+    eight products: off by 2^-10 of the products' magnitudes at most, about 2^-16 as a
+    rule, before the rounding to bf16.  With `fp32_sums` bf16 results are sums in fp32
+    too, in about twice the time."""
     p = len(X)
     _need(p >= 1, "X: no shards given")
     M, K = _matrix("X[0]", X[0], "[M, K]")
@@ -1015,7 +1027,7 @@ def fp8_matmul(X: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor], W: S
     Y = _result("Y", Y, out_dtype, (M, N), dev, stream)
     h, sp = _ctx(handle, dev, stream)
     check(load().tpf_scaled_matmul(h, p, M, K, N, *xat, *wat, kind, 1 if gelu else 0, Y.data_ptr(),
-                                   _dtype_code(Y.dtype), sp))
+                                   _sum_code(Y.dtype, fp32_sums), sp))
     return Y
 
 
@@ -1047,16 +1059,17 @@ def _results(name: str, dW, p: int, dtype, shape, dev, stream):
 
 def fp8_weight_grad(A: Sequence[torch.Tensor], a_scales: Sequence[torch.Tensor], B: Sequence[torch.Tensor],
                     b_scales: Sequence[torch.Tensor], out_dtype=torch.float32, dW=None,
-                    handle: Optional[Handle] = None, stream=None) -> List[torch.Tensor]:
+                    handle: Optional[Handle] = None, stream=None, fp32_sums: bool = False) -> List[torch.Tensor]:
     """dW[k] = A_k B_k^T for every shard k: `weight_grad` of operands in 8 bits.
 
     A[k], a_scales[k]: [R, Mt] and B[k], b_scales[k]: [C, Mt], the inputs and the
     outputs' gradients as `fp8_pack` leaves them by columns.  Row-parallel: B of
-    one gradient, p times; column-parallel: A of one input, p times."""
+    one gradient, p times; column-parallel: A of one input, p times.  bf16 results
+    and `fp32_sums` as in `fp8_matmul`."""
     dev, p, Mt, R, C, aat, bat = _weight_grad_operands(A, a_scales, B, b_scales)
     dW, wat = _results("dW", dW, p, out_dtype, (R, C), dev, stream)
     h, sp = _ctx(handle, dev, stream)
-    check(load().tpf_scaled_weight_grad(h, p, Mt, R, C, *aat, *bat, wat, _dtype_code(dW[0].dtype), sp))
+    check(load().tpf_scaled_weight_grad(h, p, Mt, R, C, *aat, *bat, wat, _sum_code(dW[0].dtype, fp32_sums), sp))
     return dW
 
 
@@ -1118,13 +1131,13 @@ def expert_route_backward(dweights: torch.Tensor, logits: torch.Tensor, route: E
 def expert_matmul(X: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor], W: Sequence[torch.Tensor],
                   w_scales: Sequence[torch.Tensor], route: ExpertRoute, gather: bool = False, gelu: bool = False,
                   out_dtype=torch.bfloat16, Y: Optional[torch.Tensor] = None, handle: Optional[Handle] = None,
-                  stream=None) -> torch.Tensor:
+                  stream=None, fp32_sums: bool = False) -> torch.Tensor:
     """The experts' products: row r of expert e becomes Y[r] = sum_k x W_k[e]^T (Y
     [T k, N]; rows of no expert are zeros), GeLU of it with `gelu`.
 
     X[k], x_scales[k]: rows as `fp8_pack` leaves them, [T k, K] in the route's
     order, or with `gather` those of the tokens, [T, K]; W[k] [E, N, K], w_scales[k]
-    [E, ceil(N/128), ceil(K/128)] as `fp8_matmul` takes them."""
+    [E, ceil(N/128), ceil(K/128)] as `fp8_matmul` takes them, and `fp32_sums` as there."""
     p = len(X)
     _need(p >= 1, "X: no shards given")
     M, K = _matrix("X[0]", X[0], "[T, K]" if gather else "[T k, K]")
@@ -1143,22 +1156,22 @@ def expert_matmul(X: Sequence[torch.Tensor], x_scales: Sequence[torch.Tensor], W
     h, sp = _ctx(handle, dev, stream)
     check(load().tpf_expert_matmul(h, p, T * k, K, N, E, *xat, *wat, kind, route.offsets.data_ptr(),
                                    route.src.data_ptr(), k if gather else 0, 1 if gelu else 0, Y.data_ptr(),
-                                   _dtype_code(Y.dtype), sp))
+                                   _sum_code(Y.dtype, fp32_sums), sp))
     return Y
 
 
 def expert_weight_grad(A: Sequence[torch.Tensor], a_scales: Sequence[torch.Tensor], B: Sequence[torch.Tensor],
                        b_scales: Sequence[torch.Tensor], route: ExpertRoute, out_dtype=torch.float32, dW=None,
-                       handle: Optional[Handle] = None, stream=None) -> List[torch.Tensor]:
+                       handle: Optional[Handle] = None, stream=None, fp32_sums: bool = False) -> List[torch.Tensor]:
     """dW[k] [E, R, C]: `fp8_weight_grad` over each expert's rows by itself, of
-    operands that `fp8_pack` packed by columns with this route."""
+    operands that `fp8_pack` packed by columns with this route; `fp32_sums` as there."""
     dev, p, Mt, R, C, aat, bat = _weight_grad_operands(A, a_scales, B, b_scales)
     T, k, E = _check_route(route, dev)
     _need(Mt == fp8_columns(T * k, E), f"A[0] has {Mt} columns, expected {fp8_columns(T * k, E)} of the route")
     dW, wat = _results("dW", dW, p, out_dtype, (E, R, C), dev, stream)
     h, sp = _ctx(handle, dev, stream)
     check(load().tpf_expert_weight_grad(h, p, Mt, R, C, E, *aat, *bat, route.offsets.data_ptr(), wat,
-                                        _dtype_code(dW[0].dtype), sp))
+                                        _sum_code(dW[0].dtype, fp32_sums), sp))
     return dW
 
 
