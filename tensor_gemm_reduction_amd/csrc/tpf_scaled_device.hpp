@@ -42,9 +42,30 @@ __device__ __forceinline__ f32x4_t sc_mfma_fine(const ScFine& w, const ScFine& x
   for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.k[i], x.k[i], c, 0, 0, 0);
   return c;
 }
-// GeLU, x Phi(x), to a few roundings of fp32.
+// GeLU, x Phi(x).  For bf16 results the density's exponent x^2 / 2 is rounded to
+// fp32, which costs up to 2^-17 of the result by x = -13.  For fp32 results what the
+// square and its product with log2(e) / 2 lose is carried into the density: 2^-20 of
+// the result at most (mills' sum and reciprocal, exp2 and four products: 7.4 half
+// steps with exact reciprocals and exp2).  Results below the least normal number may
+// be zeros.
+template <int OUT>
+__device__ __forceinline__ float sc_gelu1(float x) {
+  if constexpr (OUT == OUT_F32) {
+    const float a = fabsf(x);
+    if (a > 32.0f) return x > 0.0f ? x : x * 0.0f;
+    constexpr float kHalf = -0x1.715476p-1f, kHalfLow = -0x1.4ae0cp-27f;        // -log2(e) / 2
+    const float square = a * a, low = __builtin_fmaf(a, a, -square), t = square * kHalf;
+    const float rest = __builtin_fmaf(low, kHalf, __builtin_fmaf(square, kHalfLow, __builtin_fmaf(square, kHalf, -t)));
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float tail = mills<1>(a) * __builtin_fmaf(e, rest * 0.69314718f, e) * a;
+    return x < 0.0f ? -tail : x - tail;
+  } else {
+    return x * gauss<1>(x).cdf;
+  }
+}
+template <int OUT>
 __device__ __forceinline__ f32x4_t sc_gelu(f32x4_t v) {
-  return f32x4_t{v[0] * gauss<1>(v[0]).cdf, v[1] * gauss<1>(v[1]).cdf, v[2] * gauss<1>(v[2]).cdf, v[3] * gauss<1>(v[3]).cdf};
+  return f32x4_t{sc_gelu1<OUT>(v[0]), sc_gelu1<OUT>(v[1]), sc_gelu1<OUT>(v[2]), sc_gelu1<OUT>(v[3])};
 }
 // 2^(e - 127), NaN for 255 as the matrix instruction takes it
 __device__ __forceinline__ float exp_byte(int e) {

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(64 * W) void scaled_few_kernel(ScaledArgs args) {
     for (int w = 1; w < W; ++w) v += part[w][t][l];
     const int row = t / TN * 16 + (l & 15), col = n0 + t % TN * 16 + 4 * (l >> 4);
     if (row >= rows || col >= a.N) continue;
-    if (a.gelu) v = sc_gelu(v);
+    if (a.gelu) v = sc_gelu<OUT>(v);
     const int64_t at = (int64_t)(row0 + row) * a.N + col;
     if constexpr (OUT == OUT_F32)
       *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.y[0]) + at) = v;

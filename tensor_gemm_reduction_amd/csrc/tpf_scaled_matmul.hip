@@ -522,7 +522,7 @@ __global__ __launch_bounds__(Cfg::THREADS, 2) void scaled_tile_kernel(ScaledArgs
 #pragma unroll
     for (int n = 0; n < Cfg::TN; n += 2) {
       f32x4_t v[2] = {acc[m][n], acc[m][n + 1]};
-      if ((MODE == PLAIN || MODE == EXPERTS) && a.gelu) v[0] = sc_gelu(v[0]), v[1] = sc_gelu(v[1]);
+      if ((MODE == PLAIN || MODE == EXPERTS) && a.gelu) v[0] = sc_gelu<OUT>(v[0]), v[1] = sc_gelu<OUT>(v[1]);
       const int col0 = wn * Cfg::WN + n * 16;
       if constexpr (OUT == OUT_F32) {
 #pragma unroll

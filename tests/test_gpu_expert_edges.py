@@ -250,6 +250,42 @@ def test_factors_that_are_special(M, K, N, out):
                            want[rows].nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30))
 
 
+def gelu_operands(rows, N):
+    """Operands whose sums are exact, i + j / 16 + n / 256 from -13 to 4: (x, xs, w, ws, the sums)."""
+    x, w = torch.zeros(rows, 16), torch.zeros(N, 16)
+    whole, part = torch.arange(rows) % 17 - 13, torch.arange(rows) // 17 % 16
+    x[:, 0], x[:, 1], x[:, 2] = whole, part, 1.0
+    w[:, 0], w[:, 1], w[:, 2] = 1.0, 1.0 / 16, torch.arange(N) % 16 / 256
+    one = lambda *s: torch.full(s, 127, dtype=U8)
+    u = x.to(D) @ w.to(D).t()
+    assert torch.equal(x.to(F8).to(D) @ w.to(F8).to(D).t(), u)
+    return x.to(F8), one(rows, 4), w.to(F8), one(O.blocks(N), 1), u
+
+
+@pytest.mark.parametrize("M,N", [(272, 16), (816, 1032)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_gelu_of_far_values(M, N, out):
+    """Relative to GeLU itself, of few rows and on tiles.  fp32: 16 half steps of fp32 (2^-20), for the reciprocal, exp2
+    and products and sums of their fp32 values; bf16: 2^-16 for the square's rounding in the exponent."""
+    x, xs, w, ws, u = gelu_operands(M, N)
+    y = tp.fp8_matmul([x.cuda()], [xs.cuda()], [w.cuda()], [ws.cuda()], gelu=True, out_dtype=out).cpu().to(D)
+    want = O.gelu(u)
+    own = 2.0 ** -20 if out == F32 else O.half_step(BF) + 2.0 ** -16
+    assert ((y - want).abs() <= want.abs() * own).all()
+
+
+def test_gelu_of_extreme_values():
+    x = torch.zeros(9, 16)
+    x[:, 0] = torch.tensor([448.0, -448.0, 0.0, -0.0, 20.0, -20.0, 8.0, -8.0, 1.0])
+    x, w = x.to(F8), torch.eye(8, 16).to(F8)
+    for out in (BF, F32):
+        for scale in (127, 245):            # 2^118 of them: beyond what the square can hold
+            xs, ws = torch.full((9, 4), scale, dtype=U8), torch.full((1, 1), 127, dtype=U8)
+            y = tp.fp8_matmul([x.cuda()], [xs.cuda()], [w.cuda()], [ws.cuda()], gelu=True, out_dtype=out).cpu().to(D)[:, 0]
+            want = O.gelu(torch.ldexp(x[:, 0].to(D), torch.tensor(scale - 127)))
+            assert ((y - want).abs() <= want.abs() * (2.0 ** -16 + O.half_step(out)) + 1e-37).all()
+
+
 # ---------------------------------------------------------------------------
 # sums in fp32
 # ---------------------------------------------------------------------------
