@@ -11,6 +11,12 @@ MLP beside them, its products in 8 bits.
 
 `ExpertBlock.forward` keeps y, u_k and the experts' rows, `backward` uses them;
 `step` runs the block for the few tokens of a decode step.
+
+Precision: experts' and shared products have operands in 8 bits, and bf16 results
+that the 8-bit matrix instructions sum (`tpfuse.fp8_matmul`); their weight gradients
+are fp32.  The router's logits are fp32 sums of bf16 products; their gradient, fp32
+as well, is rounded to bf16 (2^-9 of each value) before the products that give Wr's
+and y's gradients, whose operands are bf16 as all the block's other gradients are.
 """
 from __future__ import annotations
 
@@ -138,7 +144,7 @@ class ExpertBlock:
         y, logits, route, rows, u, v, b, x_out, stats = kept
         dx, db, dw_pre, dw_post, dgate = tp.block_norm_backward(dy_next, dx_out, x_out, b, stats, **self.norm)
         drows, dweights = tp.expert_combine_backward(db, rows, route)
-        dlogits = tp.expert_route_backward(dweights, logits, route, **self.weighing).bfloat16()
+        dlogits = tp.expert_route_backward(dweights, logits, route, **self.weighing).bfloat16()     # as the products take it
         dWr, = tp.weight_grad([y], [dlogits])
         dyr, dW1, dW2 = self.experts.backward(drows, y, u, route)
         dy = tp.expert_combine(dyr, route._replace(weights=torch.ones_like(route.weights)), out_dtype=torch.float32)
