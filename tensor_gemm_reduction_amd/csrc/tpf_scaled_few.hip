@@ -164,16 +164,22 @@ hipError_t launch_few(ScaledArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Four waves a workgroup, so that three workgroups share a compute unit and one's
-// start and end lie beside the others' streams (16 tokens to 8 of 64 experts, K
-// 4096, N 1024: 49 us, with eight waves 62; 1 x 8192 x 8192: 14.8 against 17.4).
-// Eight where they read whole rows of the weights, or where there are few columns
-// (16 x 8 x 1024 x 8192: 15.5 against 16.6).
+// Eight waves a workgroup where each compute unit has one at most, four where they
+// are more: three then share a compute unit, and one's start and end lie beside the
+// others' streams.  us, four and eight waves, 1 row and 16: 8192 x 8192 (256
+// workgroups) 19.9 and 21.2, 21.4 and 20.6; 8192 x 8 x 1024 20.7 and 15.1, 21.1 and
+// 16.8; 7168 x 7168 17.1 and 12.7, 18.1 and 14.9; 8192 x 4096 11.2 and 11.2, 11.7 and
+// 11.5; more of them: 10240 x 8192 24.3 and 31.3, 30.3 and 34.5; 12288 x 4096 14.4 and
+// 17.1, 17.5 and 19.5; 16384 x 8 x 1024 28.4 and 27.9, 32.2 and 30.8; 16384 x 1024 5.7
+// and 6.7, 6.2 and 7.3.  From a block a wave on: 4096 x 1024 (8 blocks) 4.2 and 4.1,
+// 4.7 and 4.5; 4096 x 512 (4) 2.9 and 3.0, 3.1 and 3.2.  Experts' workgroups are more
+// than the compute units as a rule: 16 tokens to 8 of 64, K 4096, N 1024: 49, with eight
+// waves 62.
 template <int TM, int EXPERTS, int WS>
 hipError_t launch_few_sized(const ScaledArgs& a, hipStream_t s) {
   if constexpr (!EXPERTS) {
-    const int64_t kbs = scale_blocks(a.K);
-    if (a.p * kbs >= 16 && (kbs <= 8 || a.N <= 2048)) return launch_few<TM, 2, 8, EXPERTS, WS>(a, s);
+    const int64_t groups = ((int64_t)a.M + 16 * TM - 1) / (16 * TM) * ((a.N + 31) / 32);
+    if (a.p * scale_blocks(a.K) >= 8 && groups <= 256) return launch_few<TM, 2, 8, EXPERTS, WS>(a, s);
   }
   return launch_few<TM, 2, 4, EXPERTS, WS>(a, s);
 }
@@ -190,12 +196,16 @@ hipError_t launch_few_sized(const ScaledArgs& a, hipStream_t s) {
 // them once (16384 x 4096, M 32: 23 and 29).  Up to 16 rows read them once whatever
 // their width (28672 x 8192: 52 and 58 at M 1, 60 and 59 at M 16).
 //
-// Of experts at most M have rows.  With 32 blocks or more along the contraction
-// this kernel wins up to 8 rows an expert (8 x 4096 x 4096, 4 each: 33 and 44; 64 x
-// 1024 x 4096, 2 each: 55 and 57, 16 each: 86 and 67); with fewer, while its
-// workgroups, whose streams are short, are not many more than run at once (8 of 64 x
-// 4096 x 1024, one token: 12 and 18, 8 tokens: 50 and 47; 8 of 256 x 512 x 2048, one
-// token: 9 and 16, 8: 19 and 21, 2 rows each of all: 69 and 51).
+// Of experts at most M have rows.  Up to 8 rows an expert this kernel wins with 32
+// blocks or more along the contraction (64 x 1024 x 4096: 2 rows each 51 and 58, 8 57
+// and 67, 12 63 and 67; of 5120: 2 61 and 63, 6 69 and 67, 8 72 and 67; 64 x 2048 x 4096: 8
+// 109 and 130; 16 x 2048 x 4096: 8 36 and 37, 12 37 and 37); with fewer, while its
+// workgroups, whose streams are short, are not many more than run at once: 2048 of the
+// experts that can have rows (64 x 1024 x 3968, 31 blocks: 1024 of them 32 and 33, 2048
+// 53 and 52, with 8 rows each 56 and 52; of 2048: 1024 18 and 19, 2048 30 and 29; 8 x 8192
+// x 1024: 2048 17 and 23; 64 x 4096 x 1024: 1024 12 and 17, 2048 19 and 18, 4096 34 and
+// 30; 256 x 512 x 2048: 512 12 and 19, 2048 34 and 29, 4096 61 and 54).  Between the sizes
+// that it fits, the rule is up to 17 % off.
 int scaled_few_tiles(int64_t M, int64_t N, int64_t blocks, int64_t E) {
   const int64_t across = (N + 31) / 32;
   if (E) return M <= 8 * E && (blocks >= 32 || std::min(M, E) * across <= 2048) ? 1 : 0;

@@ -570,7 +570,12 @@ hipError_t launch_cfg(ScaledArgs a, hipStream_t s) {
 //     end beside the other's steps (so 700 where an expert's gradient sums up to
 //     1024 rows), against half again the loads;
 //   128 x 128, two a compute unit: 1 each and 110 for the start and the end.
-// An expert's last tile counts as half full.  Measured, us, in this order: 4096 x
+// An expert's last tile counts as half full.  Where gradients change from 128 x 256 to
+// 256 x 256, at 1024 rows an expert (us, 256 x 256 and 128 x 256): 16 of 4096 x 1024, 768
+// rows 89 and 83, 1024 106 and 103, 1152 112 and 112, 1280 119 and 120, 2048 164 and 166;
+// 64 of 1024 x 1024, 512 81 and 79, 1024 115 and 116, 1280 130 and 134, 2048 177 and 184; 4 of
+// 4096 x 4096, 1024 85 and 82, 1280 96 and 95, 1536 112 and 116; but 8 of 2048 x 2048, 1280
+// 56 and 52, 2560 89 and 89, 4096 138 and 148.  Measured, us, in this order: 4096 x
 // 4096 x 4096: 60, 69, 77; 2560 x 4096: 53, 58, 58; 2048 x 4096: 52, 46, 42; 4352 x
 // 4096, two rounds: 97, 88, 89.  64 experts of K 1024, N 4096, rows drawn evenly,
 // 128 each: 103, 96, 107, 512: 219, 209, 257, drawn with a power of -0.7: 226, 207,

@@ -250,6 +250,20 @@ def test_factors_that_are_special(M, K, N, out):
                            want[rows].nan_to_num(nan=1e30, posinf=2e30, neginf=-2e30))
 
 
+# workgroups up to the compute units' number and above it, of as many blocks as waves and fewer
+@pytest.mark.parametrize("p,M,K,N", [(1, 3, 1040, 8192), (1, 16, 1040, 8200), (2, 1, 528, 8264), (2, 16, 400, 8264), (1, 5, 400, 520),
+                                     (1, 33, 1040, 264), (1, 30, 1040, 8200), (3, 64, 400, 2056)])
+@pytest.mark.parametrize("kind", ["u8", "f32"])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_few_rows_of_wide_results(p, M, K, N, kind, out):
+    g = gen("wide", p, M, K)
+    x, xs = integer_packed(g, M, K, p)
+    w, ws = weights(g, p, (N, K), kind, integer=True)
+    y = tp.fp8_matmul(cuda(x), cuda(xs), cuda(w), cuda(ws), out_dtype=out)
+    want = sum(O.values(x[k], xs[k]) @ O.weight(w[k], ws[k]).t() for k in range(p))
+    assert torch.equal(y.cpu(), want.to(out))
+
+
 def gelu_operands(rows, N):
     """Operands whose sums are exact, i + j / 16 + n / 256 from -13 to 4: (x, xs, w, ws, the sums)."""
     x, w = torch.zeros(rows, 16), torch.zeros(N, 16)
