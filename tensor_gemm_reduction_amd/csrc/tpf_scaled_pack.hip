@@ -224,7 +224,9 @@ __global__ __launch_bounds__(256, 4) void scaled_pack_columns_kernel(PackArgs ar
 }  // namespace
 
 hipError_t launch_scaled_pack(const PackArgs& a, hipStream_t s) {
-  const bool together = a.codes[0] && a.codes_t[0] && !a.offsets;      // the columns' rows are the rows as they lie
+  // One read of u where the columns' rows are the rows as they lie; experts' blocks begin inside the rows' own and end
+  // before the rows of no expert, so theirs are two passes (32768 x 4096 of 64 experts: 171 us; plain rows 145).
+  const bool together = a.codes[0] && a.codes_t[0] && !a.offsets;
   if (a.codes[0] && !together) {
     const int64_t units = (int64_t)a.M * (scale_width(a.K) / 4);
     hipLaunchKernelGGL(scaled_pack_rows_kernel, dim3((unsigned)std::min<int64_t>((units + 3) / 4, 1 << 22), a.p), dim3(256),
