@@ -362,8 +362,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
 // way still (choice and order of 16384 tokens to 8 of 16: 14 us, in 64 bits 48), with
 // more experts (k from 14 on of 60: 55 to 78 us) it is not.
 // 16384 tokens, 256 experts in 8 groups with bias: 88 us with everything in 64 bits
-// and a round over all values for each choice, 20 this way (bound by the
-// instructions of about 2000 cycles a wave and by their first fetch).
+// and a round over all values for each choice, 20 this way (bound by vector
+// instructions of about 5100 cycles a wave and by their first fetch).
 constexpr int kRouteList = 32;
 // A value and its expert as one number that is compared: larger values first, the
 // lower number first among equals.

@@ -22,11 +22,11 @@
 // fp32 (FINE), take the bf16 instructions, at half the rate: codes are exact in
 // bf16 and those sums keep fp32's bits.
 //
-// What bounds them: 4 x 4096 x 4096 x 4096 take 201 us, 2730 TFLOP/s; the matrix
+// What bounds them: 4 x 4096 x 4096 x 4096 take 209 us, 2630 TFLOP/s; the matrix
 // cores are busy 64 % of the time at the 1.9 GHz that the board holds them to (a
-// library's product with one scale a tensor: 0.84 of the time).  With few steps a
+// library's product with one scale a tensor: 0.83 of the time).  With few steps a
 // tile (64 experts, K 1024) its start, first loads and stores are as long as its
-// products: 189 us, matrix cores 30 %.  Four waves of 128 x 128 would read a third
+// products: 196 us, matrix cores 29 %.  Four waves of 128 x 128 would read a third
 // less of LDS, but their sums leave too few registers (3.3 times as long).
 //
 // The weights are the instruction's first operand: lane l's four results are

@@ -14,15 +14,17 @@ D = torch.float64
 # routing
 # ---------------------------------------------------------------------------
 
-@pytest.mark.parametrize("E,groups,tops,k", [(32, 8, 3, 4), (256, 8, 4, 8), (1024, 16, 5, 8)])
+@pytest.mark.parametrize("E,groups,tops,k", [(32, 2, 1, 4), (32, 8, 3, 4), (256, 2, 1, 8), (256, 8, 4, 8), (1024, 2, 1, 8), (1024, 16, 5, 8)])
 @pytest.mark.parametrize("size", [32.0, 1000.0, 1e4])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_groups_of_biases_that_cancel(E, groups, tops, k, size, score):
     """A group's two largest near +B and -B, their sum near 1: the sum's error is that of its terms."""
     T, n = 16384 if E < 1024 else 4096, E // groups
     g = gen("cancel", E, size)
-    # from equal sums to sums that a step of fp32 near B tells apart
-    x = torch.randn(T, 1, generator=g) + torch.randn(T, E, generator=g) * torch.exp2(-24.0 * torch.rand(T, 1, generator=g))
+    # every fourth token from nearly equal sums to sums that a step of fp32 near B tells apart; the others far apart, so
+    # that they do not send the wave's four to the sums in 64 bits
+    x = torch.randn(T, E, generator=g)
+    x[::4] = x[::4, :1] + x[::4] * torch.exp2(-20.0 * torch.rand(T // 4, 1, generator=g))
     bias = torch.full((E,), -4.0 * size)
     bias[::n], bias[1::n] = size, -size
     r = tp.expert_route(x.cuda(), k, score=score, bias=bias.cuda(), groups=groups, top_groups=tops)
@@ -57,6 +59,20 @@ def test_route_with_biases_of_no_number(E, k, groups, tops, at, score):
     assert torch.equal(r.ids.cpu(), ids)
     for got, want in zip((r.offsets, r.src, r.pos), O.order(ids, E)):
         assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("E,k,groups,tops", [(64, 8, 1, 1), (61, 5, 1, 1), (32, 6, 8, 3), (256, 8, 8, 2), (1024, 16, 16, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [float("inf"), 3e38])
+def test_route_with_biases_beyond_any_score(E, k, groups, tops, score, size):
+    """Experts that are always or never taken, a group's sum among them that fp32 cannot hold."""
+    g = gen("infinite bias", E, k)
+    x = torch.randn(60, E, generator=g)
+    sign = torch.randint(-1, 2, (E,), generator=g)
+    bias = torch.where(sign == 0, 0.1 * torch.randn(E, generator=g), sign * size)
+    for b in (bias, bias.clamp(max=1.0), bias.clamp(min=-1.0), torch.full((E,), -size)):
+        r = tp.expert_route(x.cuda(), k, score=score, bias=b.cuda(), groups=groups, top_groups=tops)
+        assert torch.equal(r.ids.cpu(), O.choose(x, k, score, b, groups, tops, None))
 
 
 @pytest.mark.parametrize("E,k,groups,tops", [(8, 3, 1, 1), (8, 8, 1, 1), (16, 8, 1, 1), (31, 16, 1, 1), (32, 16, 1, 1),
