@@ -455,7 +455,7 @@ int64_t tpf_expert_columns(int64_t R, int64_t E);
 /* Y = sum_k X[k] W_k^T, row-parallel over the shards (p = 1: any Linear).
  *   X[k], x_scales[k]: [M, K] packed.
  *   W[k]: [N, K] codes; w_scales[k]: [ceil(N/128), ceil(K/128)] of w_scale_type.
- *   Y: [M, N] of y_dtype; with gelu != 0 GeLU of the fp32 sum.
+ *   Y: [M, N] of y_dtype; with gelu != 0 GeLU of the sum.
  * N must be a multiple of 8, x_scales 4-byte aligned, w_scales as their type. */
 int tpf_scaled_matmul(tpf_handle h, int p, int64_t M, int64_t K, int64_t N, const void* const* X,
                       const void* const* x_scales, const void* const* W, const void* const* w_scales,
@@ -507,7 +507,8 @@ int tpf_expert_route(tpf_handle h, int64_t T, int64_t E, int k, const void* logi
 size_t tpf_expert_route_ws(int64_t T, int64_t E);
 
 /* Gradient of the logits ([T, E] of dtype) from that of the weights ([T, k]
- * fp32), the choice held; ids and weights as tpf_expert_route left them. */
+ * fp32), the choice held; ids and weights as tpf_expert_route left them (with
+ * renorm a token's weights sum to scale). */
 int tpf_expert_route_backward(tpf_handle h, int64_t T, int64_t E, int k, const void* logits, int dtype, int score,
                               int renorm, double scale, const int32_t* ids, const float* weights,
                               const float* dweights, void* dlogits, void* stream);

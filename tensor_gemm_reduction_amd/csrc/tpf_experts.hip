@@ -444,8 +444,8 @@ __global__ __launch_bounds__(kRouteThreads) void expert_route_kernel(RouteArgs a
   const bool softmax = a.score == SCORE_SOFTMAX, scores = a.bias || a.groups > 1;
   const int gs = a.E / a.groups, gs_inv = ((1 << 20) + gs - 1) / gs;
   // Groups of whole fours take the fast way, and any number of experts without groups (but see k above); other groups
-  // are routed in 64 bits by the whole wave (16384 tokens: 6 of 128 17 us, of 129 by single loads 19, in 64 bits 47; 6 of 64 in 4
-  // groups 17, of 60 49).
+  // are routed in 64 bits by the whole wave (16384 tokens: 6 of 128 17 us, of 129 by single loads 19, in 64 bits 47;
+  // 6 of 64 in 4 groups 17, of 60 49).
   const bool whole = a.E % 4 == 0, fours = a.groups == 1 || (whole && gs % 4 == 0);
   // Twice the largest error of an fp32 value v is below bound (1 + |v|): sigmoid 4e-7 (exp2, reciprocal and sum
   // round by 1.2e-7 at most, the argument's rounding counts s (1 - s) |x| 2^-24), softmax 2.4e-6 (a sum of 1024).

@@ -68,9 +68,11 @@ __global__ __launch_bounds__(64 * W) void scaled_few_kernel(ScaledArgs args) {
   const int64_t x_bytes = (int64_t)(gather ? a.xrows : rows) * a.K, w_bytes = (int64_t)min(16 * TN, a.N - n0) * a.K;
   const int64_t ws_at = ((int64_t)e * ((a.N + kScaleBlock - 1) / kScaleBlock) + n0 / kScaleBlock) * a.wsw;
 
-  // The next block to be loaded.  Tiles start at blocks of their own: from the same one, rows whose length is a power
-  // of two would all be read from the same few memory channels.
-  const int b0 = blocks ? (int)((uint32_t)(wave + (n0 / (16 * TN) + unit) * W) % (uint32_t)blocks) : 0;
+  // The next block to be loaded.  Tiles start at blocks of their own, W + 1 apart: from the same one, or from the few
+  // that steps of W leave of a power of two, rows of such a length would all be read from the same few memory channels
+  // (8192 x 8192, 1 row: steps of W 21.2 us, of W + 1 15.1; 4096 x 8192 11.2 and 9.0; 28672 x 2048, four waves, 14.2
+  // and 15.1).
+  const int b0 = blocks ? (int)((uint32_t)(wave + (n0 / (16 * TN) + unit) * (W + 1)) % (uint32_t)blocks) : 0;
   int s = b0 / kbs, kb = b0 - s * kbs;
   const auto load = [&](FewBlock<TM, TN>& b) {
     const int k0 = kb * kScaleBlock;
@@ -167,14 +169,14 @@ hipError_t launch_few(ScaledArgs a, hipStream_t s) {
 // Eight waves a workgroup where each compute unit has one at most, four where they
 // are more: three then share a compute unit, and one's start and end lie beside the
 // others' streams.  us, four and eight waves, 1 row and 16: 8192 x 8192 (256
-// workgroups) 19.9 and 21.2, 21.4 and 20.6; 8192 x 8 x 1024 20.7 and 15.1, 21.1 and
-// 16.8; 7168 x 7168 17.1 and 12.7, 18.1 and 14.9; 8192 x 4096 11.2 and 11.2, 11.7 and
-// 11.5; more of them: 10240 x 8192 24.3 and 31.3, 30.3 and 34.5; 12288 x 4096 14.4 and
-// 17.1, 17.5 and 19.5; 16384 x 8 x 1024 28.4 and 27.9, 32.2 and 30.8; 16384 x 1024 5.7
-// and 6.7, 6.2 and 7.3.  From a block a wave on: 4096 x 1024 (8 blocks) 4.2 and 4.1,
-// 4.7 and 4.5; 4096 x 512 (4) 2.9 and 3.0, 3.1 and 3.2.  Experts' workgroups are more
-// than the compute units as a rule: 16 tokens to 8 of 64, K 4096, N 1024: 49, with eight
-// waves 62.
+// workgroups) 20.3 and 15.1, 21.7 and 17.1; 8192 x 8 x 1024 19.5 and 14.9, 20.3 and
+// 16.2; 7168 x 7168 17.2 and 12.7, 18.2 and 14.8; 8192 x 4096 10.4 and 9.0, 11.3 and
+// 10.4; more of them: 10240 x 8192 24.7 and 25.0, 30.2 and 31.0; 12288 x 4096 13.4 and
+// 15.1, 17.3 and 18.0; 16384 x 8 x 1024 26.6 and 27.5, 29.8 and 30.7; 16384 x 1024 5.8
+// and 6.7, 6.1 and 7.2; 28672 x 8192 54.1 and 50.3, 59.1 and 60.7.  From a block a wave
+// on: 4096 x 1024 (8 blocks) 4.2 and 4.1, 4.7 and 4.5; 4096 x 512 (4) 2.9 and 3.0, 3.1
+// and 3.2.  Experts' workgroups are more than the compute units as a rule: 16 tokens to
+// 8 of 64, K 4096, N 1024: 49, with eight waves 62.
 template <int TM, int EXPERTS, int WS>
 hipError_t launch_few_sized(const ScaledArgs& a, hipStream_t s) {
   if constexpr (!EXPERTS) {

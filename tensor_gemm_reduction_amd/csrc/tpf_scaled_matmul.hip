@@ -6,7 +6,7 @@
 // rows' exponent bytes go into the instruction and a product of two of them
 // costs nothing beside it.  Of a weight's fp32 scale the power of two goes into the
 // instruction as well, so that no partial sum leaves fp32's range where the scales'
-// product lies within it (4096^3: 97 us as with the whole scale afterwards); its other
+// product lies within it (4096^3: 79 us as with the whole scale afterwards); its other
 // part, 1 to 2, takes one fused multiply-add an element more.
 //
 // Lane l of the instruction holds 32 codes of row (or column) l % 16.  Which 32
