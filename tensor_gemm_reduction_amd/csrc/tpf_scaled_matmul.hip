@@ -26,7 +26,7 @@
 // cores are busy 64 % of the time at the 1.9 GHz that the board holds them to (a
 // library's product with one scale a tensor: 0.83 of the time).  With few steps a
 // tile (64 experts, K 1024) its start, first loads and stores are as long as its
-// products: 196 us, matrix cores 29 %.  Four waves of 128 x 128 would read a third
+// products: 195 us, matrix cores 29 %.  Four waves of 128 x 128 would read a third
 // less of LDS, but their sums leave too few registers (3.3 times as long).
 //
 // The weights are the instruction's first operand: lane l's four results are
